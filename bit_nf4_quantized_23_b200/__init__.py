@@ -23,6 +23,7 @@ __all__ = [
     "qlora_quantize_nf4_dq",
     "qlora_quantize_nf4_dq_noalloc",
     "qlora_dequantize", "qlora_quantize_int8_absmax", "qlora_dequantize_int8_absmax", "qlora_merge_lora", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi", "qlora_linear_bwd",
+    "qlora_distill_topk_fwd", "qlora_distill_topk_bwd",
     "qlora_read_device_errors", "qlora_selftest_bounded_wait", "qlora_launch_count", "qlora_timing_enable", "qlora_timing_read",
 ]
 
@@ -345,8 +346,86 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
+def _need_here(name: str, *tensors):
+    """All tensors on the current CUDA device, where the library launches."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name}: every tensor must be on the current CUDA device cuda:{dev}, got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, shape=None):
+    """A 2-D CUDA tensor of a library dtype whose rows are contiguous; returns (dtype code, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _dtype_code(t.dtype)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}, "
+                         f"got {tuple(t.shape)}")
+    M, V = t.shape
+    ld = t.stride(0) if M > 1 else max(V, 1)
+    if not t.is_cuda or (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+    return code, ld
+
+
+def _topk_args(logits, teacher_idx, teacher_logits):
+    z_code, ld = _rows(logits, "logits")
+    if not isinstance(teacher_idx, torch.Tensor) or teacher_idx.dim() != 2:
+        raise ValueError("teacher_idx must be a 2-D tensor [M, k]")
+    k = teacher_idx.shape[1]
+    _need(teacher_idx, torch.int32, "teacher_idx", (logits.shape[0], k))
+    t_code = _dtype_code(teacher_logits.dtype)
+    _need(teacher_logits, teacher_logits.dtype, "teacher_logits", (logits.shape[0], k))
+    return z_code, ld, k, t_code
+
+
+def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,
+                           temperature: float = 1.0, loss: torch.Tensor | None = None,
+                           lse: torch.Tensor | None = None, stream=None):
+    """Distillation loss of each row from a teacher's top logits: T^2 KL(p || q), p the softmax of the
+    row's k teacher logits over T and q the student's over the whole vocabulary.  logits [M, V] (bf16,
+    fp16 or fp32, rows contiguous), teacher_idx int32 [M, k] (-1: no entry), teacher_logits [M, k].
+    Returns (loss, lse), fp32 [M]; the backward takes lse."""
+    z_code, ld, k, t_code = _topk_args(logits, teacher_idx, teacher_logits)
+    M, V = logits.shape
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=logits.device)
+    if lse is None:
+        lse = torch.empty(M, dtype=torch.float32, device=logits.device)
+    _need(loss, torch.float32, "loss", (M,))
+    _need(lse, torch.float32, "lse", (M,))
+    _need_here("qlora_distill_topk_fwd", logits, teacher_idx, teacher_logits, loss, lse)
+    check(lib().qlora_distill_topk_fwd(_ptr(logits), z_code, ld, M, V, _ptr(teacher_idx), _ptr(teacher_logits),
+                                       t_code, k, float(temperature), _ptr(loss), _ptr(lse), _stream(stream)),
+          "qlora_distill_topk_fwd")
+    return loss, lse
+
+
+def qlora_distill_topk_bwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,
+                           lse: torch.Tensor, dloss: torch.Tensor, temperature: float = 1.0, d_dtype=None,
+                           dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """d(sum_m dloss[m] loss[m]) / d logits, in d_dtype (the logits' dtype when None): the dY of the
+    output projection's backward.  `dlogits` may be `logits` itself."""
+    z_code, ld, k, t_code = _topk_args(logits, teacher_idx, teacher_logits)
+    M, V = logits.shape
+    _need(lse, torch.float32, "lse", (M,))
+    _need(dloss, torch.float32, "dloss", (M,))
+    if dlogits is None:
+        dlogits = torch.empty(M, V, dtype=logits.dtype if d_dtype is None else d_dtype, device=logits.device)
+    elif d_dtype is not None and dlogits.dtype != d_dtype:
+        raise TypeError(f"dlogits must be {d_dtype}, got {dlogits.dtype}")
+    d_code, ldd = _rows(dlogits, "dlogits", (M, V))
+    _need_here("qlora_distill_topk_bwd", logits, teacher_idx, teacher_logits, lse, dloss, dlogits)
+    check(lib().qlora_distill_topk_bwd(_ptr(logits), z_code, ld, M, V, _ptr(teacher_idx), _ptr(teacher_logits),
+                                       t_code, k, float(temperature), _ptr(lse), _ptr(dloss), _ptr(dlogits), d_code,
+                                       ldd, _stream(stream)), "qlora_distill_topk_bwd")
+    return dlogits
+
+
 def qlora_read_device_errors(clear: bool = True, stream=None) -> int:
-    """Synchronize and return the device error flags (1: timeout, 2: non-finite weight)."""
+    """Synchronize and return the device error flags (1: timeout, 2: non-finite weight,
+    4: an index out of range)."""
     f = c_uint32()
     lib().qlora_read_device_errors(_stream(stream), 1 if clear else 0, byref(f))
     return f.value

@@ -56,6 +56,10 @@ SIGNATURES = {
     "qlora_linear_bwd": (c_int32, [_W, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_float,
                                    c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
                                    c_void_p]),
+    "qlora_distill_topk_fwd": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int32,
+                                         c_int32, c_float, c_void_p, c_void_p, c_void_p]),
+    "qlora_distill_topk_bwd": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int32,
+                                         c_int32, c_float, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_void_p]),
     "qlora_read_device_errors": (c_int32, [c_void_p, c_int32, POINTER(c_uint32)]),
     "qlora_selftest_bounded_wait": (c_int32, [c_uint32, c_void_p, c_void_p]),
     "qlora_launch_count": (c_uint64, []),

@@ -1,0 +1,539 @@
+// Distillation from a teacher's top logits: the loss that trains the adapters towards a 16-bit
+// model's answers, of which only the k largest logits of each row are kept, and its gradient
+// with respect to the student's logits (the dY of the output projection's backward).
+//
+// For row m with valid entries j (0 <= i_j < V), teacher logits t_j and student logits z:
+//     p_j   = exp(t_j/T) / sum over the valid entries         (softmax over the kept logits)
+//     lse   = log sum_v exp(z_v/T)                            (over the whole vocabulary)
+//     loss  = T^2 sum_j p_j (log p_j - (z_{i_j}/T - lse))     (KL divergence, scaled by T^2)
+//     dz_v  = dloss T (exp(z_v/T - lse) - sum_{j: i_j = v} p_j)
+// A row without valid entries (none given, or every t_j = -inf) has loss 0 and gradient 0.
+//
+// Both kernels are bound by HBM: the forward reads every logit once (running maximum and sum of
+// the softmax in registers, fp32, base-2 exponentials), the backward reads and writes every
+// element once.  A row is a CTA's work; when there are too few rows to fill the GPU, the forward
+// gives a row to a cluster of up to 8 CTAs that join their (maximum, sum) pairs through
+// distributed shared memory, and the backward cuts the row into independent parts (the saved lse
+// is all that a part needs of the others).
+#include <climits>
+#include <cmath>
+
+#include <cooperative_groups.h>
+
+#include "qlora_internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTop = 1024;                     // teacher entries per row
+constexpr int kTopPerThread = kMaxTop / kThreads;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr double kLog2e = 1.4426950408889634;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int DT>
+__device__ __forceinline__ float load1(const void* base, int64_t e) {
+    if constexpr (DT == QLORA_DTYPE_F32) return static_cast<const float*>(base)[e];
+    else return from16(static_cast<const uint16_t*>(base)[e], DT == QLORA_DTYPE_F16);
+}
+
+__device__ __forceinline__ float load_any(const void* base, int64_t e, int dt) {
+    return dt == QLORA_DTYPE_F32 ? static_cast<const float*>(base)[e]
+                                 : from16(static_cast<const uint16_t*>(base)[e], dt == QLORA_DTYPE_F16);
+}
+
+template <int DT>
+__device__ __forceinline__ void store1(void* base, int64_t e, float v) {
+    if constexpr (DT == QLORA_DTYPE_F32) static_cast<float*>(base)[e] = v;
+    else static_cast<uint16_t*>(base)[e] = (uint16_t)to16_rn(v, DT == QLORA_DTYPE_F16);
+}
+
+// Eight consecutive elements as loaded (16 bytes of a 16-bit type, 32 of fp32); the address is
+// 16-byte aligned.
+template <int DT>
+struct Raw8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* base, int64_t e) {
+        if constexpr (DT == QLORA_DTYPE_F32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e);
+            a = __ldcs(p);
+            b = __ldcs(p + 1);
+        } else {
+            a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e));
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        if constexpr (DT == QLORA_DTYPE_F32) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == QLORA_DTYPE_F16) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                } else {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ void store8(void* base, int64_t e, const float (&v)[8]) {
+    if constexpr (DT == QLORA_DTYPE_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e);
+        __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+    } else {
+        constexpr bool h = DT == QLORA_DTYPE_F16;
+        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e),
+               make_uint4(pack16x2_rn(v[0], v[1], h), pack16x2_rn(v[2], v[3], h), pack16x2_rn(v[4], v[5], h),
+                          pack16x2_rn(v[6], v[7], h)));
+    }
+}
+
+// Running maximum and sum of base-2 exponentials: sum_i 2^(y_i) = s 2^m.  m = -inf stands for an
+// empty sum; the reference subtracted from the exponents is 0 then, so -inf logits add zeros and
+// never meet -inf - -inf.
+struct Softmax2 {
+    float m, s;
+    __device__ __forceinline__ static float ref(float m) { return m == -INFINITY ? 0.f : m; }
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float c) {
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+        const float mn = fmaxf(m, top * c), r = ref(mn);
+        float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            acc0 += exp2_approx(__fmaf_rn(x[i], c, -r));
+            if (i + 1 < N) acc1 += exp2_approx(__fmaf_rn(x[i + 1], c, -r));
+        }
+        s = __fmaf_rn(s, exp2_approx(m - r), acc0 + acc1);
+        m = mn;
+    }
+    __device__ __forceinline__ void join(float m2, float s2) {
+        const float mn = fmaxf(m, m2), r = ref(mn);
+        s = s * exp2_approx(m - r) + s2 * exp2_approx(m2 - r);
+        m = mn;
+    }
+};
+
+struct DistillParams {
+    const void* logits;       // [M, V], rows ld elements apart
+    int64_t ld;
+    int64_t M, V;
+    const int32_t* idx;       // [M, k]
+    const void* t;            // [M, k]
+    int32_t t_dtype, k;
+    float c;                  // log2(e) / T
+    float T, T2;              // T, T^2
+    float* loss;              // [M]            (forward)
+    float* lse;               // [M]            (written by the forward, read by the backward)
+    const float* dloss;       // [M]            (backward)
+    void* dlogits;            // [M, V], rows ldd elements apart
+    int64_t ldd;
+    int32_t parts;            // CTAs of a row
+    uint32_t* err;
+};
+
+__device__ __forceinline__ float block_max(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = red[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) r = fmaxf(r, red[w]);
+    __syncthreads();
+    return r;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) r += red[w];
+    __syncthreads();
+    return r;
+}
+
+// The teacher entries of thread tid in row m: e = tid + 256 q.  An index outside [0, V) is no
+// entry; one at or above V raises the BOUNDS flag too.
+struct Top {
+    int32_t i[kTopPerThread];
+    float t[kTopPerThread];    // teacher logit (-inf: no entry); then log2 p
+};
+__device__ __forceinline__ void load_top(const DistillParams& p, int64_t m, Top& top) {
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) {
+        const int e = threadIdx.x + q * kThreads;
+        top.i[q] = -1;
+        top.t[q] = -INFINITY;
+        if (e < p.k) {
+            const int32_t i = p.idx[m * p.k + e];
+            if (i >= 0 && i < p.V) {
+                top.i[q] = i;
+                top.t[q] = load_any(p.t, m * p.k + e, p.t_dtype);
+            } else if (i >= 0) {
+                atomicOr(p.err, ERR_FLAG_BOUNDS);
+            }
+        }
+    }
+}
+
+// Turns top.t into log2 p; returns whether the row has any entry.  The differences to the row's
+// largest logit are taken before the scaling, so rows of the type's lowest value stay finite.  The
+// maximum skips NaN and the sum does not: a NaN among the row's teacher logits gives NaN.
+__device__ __forceinline__ bool teacher_log2p(Top& top, float c, float* red) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) mx = fmaxf(mx, top.t[q]);
+    mx = block_max(mx, red);
+    const float r = Softmax2::ref(mx);
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) {
+        top.t[q] = __fmul_rn(__fsub_rn(top.t[q], r), c);
+        s += exp2f(top.t[q]);
+    }
+    s = block_sum(s, red);
+    const float l = log2f(s);
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) top.t[q] = __fsub_rn(top.t[q], l);
+    return !(s == 0.f);
+}
+
+// Row layout of a part: elements [0, head) one by one, then chunks of eight from `head` on, then
+// the tail one by one; head brings the chunks to 16-byte boundaries.
+template <int DT_IN>
+__global__ void __launch_bounds__(kThreads, 4) distill_fwd(DistillParams p) {
+    grid_dependency_wait();
+    allow_dependents();
+    __shared__ float red[kWarps];
+    __shared__ float2 joined[8];
+    const int part = (int)(blockIdx.x % (unsigned)p.parts);
+    const int64_t m = blockIdx.x / (unsigned)p.parts;
+    constexpr int kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2;
+    const char* row = static_cast<const char*>(p.logits) + m * p.ld * kEs;
+
+    // a cluster's CTAs have all started before one writes another's shared memory
+    if (p.parts > 1) cg::this_cluster().barrier_arrive();
+    Top top;
+    float zt[kTopPerThread];                                  // student logits of the entries
+    if (part == 0) {
+        load_top(p, m, top);
+#pragma unroll
+        for (int q = 0; q < kTopPerThread; ++q) zt[q] = top.i[q] >= 0 ? load1<DT_IN>(row, top.i[q]) : 0.f;
+    }
+
+    const int64_t head = min(p.V, (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kEs);
+    const int64_t chunks = (p.V - head) / 8;
+    const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
+    Softmax2 acc{-INFINITY, 0.f};
+    constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 2 : 4; // 64 bytes of loads in flight per thread
+    int64_t c = c0 + threadIdx.x;
+    for (; c + (kUnroll - 1) * kThreads < c1; c += kUnroll * kThreads) {
+        Raw8<DT_IN> raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) raw[u].load(row, head + 8 * (c + u * kThreads));
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float v[8];
+            raw[u].values(v);
+            acc.add(v, p.c);
+        }
+    }
+    for (; c < c1; c += kThreads) {
+        Raw8<DT_IN> raw;
+        raw.load(row, head + 8 * c);
+        float v[8];
+        raw.values(v);
+        acc.add(v, p.c);
+    }
+    if (part == p.parts - 1) {                                // fewer than 8 + 8 single elements
+        const int64_t tail0 = head + 8 * chunks, singles = head + (p.V - tail0);
+        if (threadIdx.x < singles) {
+            const float v[1] = {load1<DT_IN>(row, threadIdx.x < head ? threadIdx.x : tail0 + (threadIdx.x - head))};
+            acc.add(v, p.c);
+        }
+    }
+
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, acc.m, o), s2 = __shfl_xor_sync(0xffffffffu, acc.s, o);
+        acc.join(m2, s2);
+    }
+    __shared__ float2 warp_acc[kWarps];
+    if ((threadIdx.x & 31) == 0) warp_acc[threadIdx.x >> 5] = make_float2(acc.m, acc.s);
+    __syncthreads();
+    acc = Softmax2{warp_acc[0].x, warp_acc[0].y};
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) acc.join(warp_acc[w].x, warp_acc[w].y);
+    if (p.parts > 1) {                                        // the row's CTAs are one cluster
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.barrier_wait();
+        if (threadIdx.x == 0) *cluster.map_shared_rank(&joined[part], 0) = make_float2(acc.m, acc.s);
+        cluster.sync();
+        if (part != 0) return;
+        acc = Softmax2{joined[0].x, joined[0].y};
+        for (int w = 1; w < p.parts; ++w) acc.join(joined[w].x, joined[w].y);
+    }
+    const float lse2 = acc.m + log2f(acc.s);
+    const bool some = teacher_log2p(top, p.c, red);
+    float part_loss = 0.f;
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) {
+        const float lp = top.t[q], pj = exp2f(lp);
+        if (top.i[q] >= 0 && !(pj == 0.f)) part_loss += pj * (lp - __fmaf_rn(zt[q], p.c, -lse2));
+    }
+    const float sum = block_sum(part_loss, red);
+    if (threadIdx.x == 0) {
+        p.lse[m] = lse2 * kLn2;
+        p.loss[m] = some ? p.T2 * kLn2 * sum : 0.f;
+    }
+}
+
+template <int DT_IN, int DT_OUT, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) distill_bwd(DistillParams p) {
+    grid_dependency_wait();
+    allow_dependents();
+    __shared__ float red[kWarps];
+    __shared__ int32_t s_i[kMaxTop];
+    __shared__ float s_p[kMaxTop];
+    const int part = (int)(blockIdx.x % (unsigned)p.parts);
+    // the rows run from the last to the first: what the forward has read last is still in L2
+    const int64_t m = p.M - 1 - blockIdx.x / (unsigned)p.parts;
+    constexpr int kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2, kEd = DT_OUT == QLORA_DTYPE_F32 ? 4 : 2;
+    const char* row = static_cast<const char*>(p.logits) + m * p.ld * kEs;
+    char* drow = static_cast<char*>(p.dlogits) + m * p.ldd * kEd;
+    // VEC: both rows are 16-byte aligned `head` elements in, for the same head in 0 .. 7
+    const int64_t head = VEC ? min(p.V, (int64_t)((8 - (m * p.ld & 7)) & 7)) : 0;
+    const int64_t chunks = VEC ? (p.V - head) / 8 : 0;
+    const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
+    const bool last = part == p.parts - 1;
+    // this part's elements: [lo, hi), and the last part's head [0, head) and tail too
+    const int64_t lo = VEC ? head + 8 * c0 : p.V * part / p.parts;
+    const int64_t hi = VEC ? (last ? p.V : head + 8 * c1) : p.V * (part + 1) / p.parts;
+
+    const float g = p.dloss[m];
+    Top top;
+    load_top(p, m, top);
+    const bool zero = !teacher_log2p(top, p.c, red) || g == 0.f;
+    const float scale = g * p.T;
+    const float l2 = __fmul_rn(p.lse[m], (float)kLog2e);
+
+    if (!zero) {
+        // the entries' values: the first of equal indices carries the sum of their probabilities
+#pragma unroll
+        for (int q = 0; q < kTopPerThread; ++q) {
+            const int e = threadIdx.x + q * kThreads;
+            if (e < p.k) {
+                s_i[e] = top.i[q];
+                s_p[e] = exp2f(top.t[q]);
+            }
+        }
+    }
+    __syncthreads();
+    float fix[kTopPerThread];
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) {
+        const int e = threadIdx.x + q * kThreads;
+        if (e >= p.k || zero) top.i[q] = -1;
+        const int32_t i = top.i[q];
+        if (i < 0 || !((i >= lo && i < hi) || (last && i < head))) { top.i[q] = -1; continue; }
+        float sum = 0.f;
+        for (int o = 0; o < p.k; ++o) {
+            if (s_i[o] != i) continue;
+            if (o < e) { top.i[q] = -1; break; }
+            sum += s_p[o];
+        }
+        // read before the row is written: the gradient may take the logits' place
+        fix[q] = scale * (exp2_approx(__fmaf_rn(load1<DT_IN>(row, i), p.c, -l2)) - sum);
+    }
+    __syncthreads();
+
+    if (VEC) {
+        constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 2 : 4;
+        int64_t c = c0 + threadIdx.x;
+        if (zero) {
+            const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (; c < c1; c += kThreads) store8<DT_OUT>(drow, head + 8 * c, v);
+        } else {
+            for (; c + (kUnroll - 1) * kThreads < c1; c += kUnroll * kThreads) {
+                Raw8<DT_IN> raw[kUnroll];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) raw[u].load(row, head + 8 * (c + u * kThreads));
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    float v[8];
+                    raw[u].values(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = scale * exp2_approx(__fmaf_rn(v[i], p.c, -l2));
+                    store8<DT_OUT>(drow, head + 8 * (c + u * kThreads), v);
+                }
+            }
+            for (; c < c1; c += kThreads) {
+                Raw8<DT_IN> raw;
+                raw.load(row, head + 8 * c);
+                float v[8];
+                raw.values(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = scale * exp2_approx(__fmaf_rn(v[i], p.c, -l2));
+                store8<DT_OUT>(drow, head + 8 * c, v);
+            }
+        }
+        if (last) {
+            const int64_t tail0 = head + 8 * chunks, singles = head + (p.V - tail0), tid = threadIdx.x;
+            if (tid < singles) {
+                const int64_t e = tid < head ? tid : tail0 + (tid - head);
+                store1<DT_OUT>(drow, e, zero ? 0.f : scale * exp2_approx(__fmaf_rn(load1<DT_IN>(row, e), p.c, -l2)));
+            }
+        }
+    } else {
+        for (int64_t e = lo + threadIdx.x; e < hi; e += kThreads)
+            store1<DT_OUT>(drow, e, zero ? 0.f : scale * exp2_approx(__fmaf_rn(load1<DT_IN>(row, e), p.c, -l2)));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q)
+        if (top.i[q] >= 0) store1<DT_OUT>(drow, top.i[q], fix[q]);
+}
+
+inline int elem_size(int dt) { return dt == QLORA_DTYPE_F32 ? 4 : 2; }
+
+// CTAs of a row: enough to give every SM two, in powers of two up to a portable cluster's eight,
+// while each still has 4096 elements (two passes of the block).
+int row_parts(int64_t M, int64_t V) {
+    int parts = 1;
+    while (parts < 8 && M * parts < 2 * 148 && V / (2 * parts) >= 4096) parts *= 2;
+    return parts;
+}
+
+template <int DT_IN>
+cudaError_t run_fwd(const DistillParams& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.M * p.parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, distill_fwd<DT_IN>, p);
+}
+
+template <int DT_IN, int DT_OUT>
+cudaError_t run_bwd2(const DistillParams& p, cudaStream_t s) {
+    const dim3 grid((unsigned)(p.M * p.parts));
+    // chunks of eight are 16-byte aligned in both rows when the row strides agree modulo eight
+    if (((p.ld ^ p.ldd) & 7) == 0) return launch_dependent(distill_bwd<DT_IN, DT_OUT, true>, grid, dim3(kThreads), 0, s, p);
+    return launch_dependent(distill_bwd<DT_IN, DT_OUT, false>, grid, dim3(kThreads), 0, s, p);
+}
+
+template <int DT_IN>
+cudaError_t run_bwd(const DistillParams& p, int d_dtype, cudaStream_t s) {
+    if (d_dtype == QLORA_DTYPE_F32) return run_bwd2<DT_IN, QLORA_DTYPE_F32>(p, s);
+    if (d_dtype == QLORA_DTYPE_F16) return run_bwd2<DT_IN, QLORA_DTYPE_F16>(p, s);
+    return run_bwd2<DT_IN, QLORA_DTYPE_BF16>(p, s);
+}
+
+bool dtype_ok(int32_t dt) { return dt == QLORA_DTYPE_BF16 || dt == QLORA_DTYPE_F16 || dt == QLORA_DTYPE_F32; }
+
+// The checks that both directions share; fills the common parameters.
+qlora_status distill_args(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V, const int32_t* idx,
+                          const void* t, int32_t t_dtype, int32_t k, float T, DistillParams& p) {
+    QLORA_TRY(check_dev(logits));
+    QLORA_TRY(check_dev(idx));
+    QLORA_TRY(check_dev(t));
+    if (!dtype_ok(z_dtype) || !dtype_ok(t_dtype)) return QLORA_ERR_INVALID_ARG;
+    if (k < 1 || k > kMaxTop) return QLORA_ERR_INVALID_ARG;
+    // 1/T^2 and T^2 stay normal fp32 numbers within these limits
+    if (!(T >= 1e-3f && T <= 1e3f)) return QLORA_ERR_INVALID_ARG;
+    if (M < 1 || V < 1 || V > INT32_MAX || ld < V || M > INT32_MAX / 8 || ld > (int64_t(1) << 40) / M)
+        return QLORA_ERR_SHAPE;
+    p.logits = logits; p.ld = ld; p.M = M; p.V = V;
+    p.idx = idx; p.t = t; p.t_dtype = t_dtype; p.k = k;
+    p.c = (float)(kLog2e / (double)T); p.T = T; p.T2 = T * T;
+    p.parts = row_parts(M, V);
+    return QLORA_OK;
+}
+
+}  // namespace
+}  // namespace qlora
+
+using namespace qlora;
+
+extern "C" {
+
+qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,
+                                    const int32_t* teacher_idx, const void* teacher_logits, int32_t t_dtype, int32_t k,
+                                    float temperature, float* loss, float* lse, void* stream) {
+    DistillParams p{};
+    QLORA_TRY(distill_args(logits, z_dtype, ld, M, V, teacher_idx, teacher_logits, t_dtype, k, temperature, p));
+    QLORA_TRY(check_dev(loss));
+    QLORA_TRY(check_dev(lse));
+    p.loss = loss; p.lse = lse;
+    p.err = device_error_word();
+    if (!p.err) return QLORA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (z_dtype == QLORA_DTYPE_F32) (void)run_fwd<QLORA_DTYPE_F32>(p, s);
+    else if (z_dtype == QLORA_DTYPE_F16) (void)run_fwd<QLORA_DTYPE_F16>(p, s);
+    else (void)run_fwd<QLORA_DTYPE_BF16>(p, s);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+qlora_status qlora_distill_topk_bwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,
+                                    const int32_t* teacher_idx, const void* teacher_logits, int32_t t_dtype, int32_t k,
+                                    float temperature, const float* lse, const float* dloss, void* dlogits,
+                                    int32_t d_dtype, int64_t ldd, void* stream) {
+    DistillParams p{};
+    QLORA_TRY(distill_args(logits, z_dtype, ld, M, V, teacher_idx, teacher_logits, t_dtype, k, temperature, p));
+    QLORA_TRY(check_dev(lse));
+    QLORA_TRY(check_dev(dloss));
+    QLORA_TRY(check_dev(dlogits));
+    if (!dtype_ok(d_dtype)) return QLORA_ERR_INVALID_ARG;
+    if (ldd < V || ldd > (int64_t(1) << 40) / M) return QLORA_ERR_SHAPE;
+    // in place (the same rows of the same type) or apart: anything between would read written values
+    const uintptr_t z0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(dlogits);
+    const uintptr_t z1 = z0 + (uintptr_t)((M - 1) * ld + V) * elem_size(z_dtype);
+    const uintptr_t d1 = d0 + (uintptr_t)((M - 1) * ldd + V) * elem_size(d_dtype);
+    const bool same = z0 == d0 && ld == ldd && elem_size(z_dtype) == elem_size(d_dtype);
+    if (!same && z0 < d1 && d0 < z1) return QLORA_ERR_INVALID_ARG;
+    p.lse = const_cast<float*>(lse); p.dloss = dloss; p.dlogits = dlogits; p.ldd = ldd;
+    p.err = device_error_word();
+    if (!p.err) return QLORA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (z_dtype == QLORA_DTYPE_F32) (void)run_bwd<QLORA_DTYPE_F32>(p, d_dtype, s);
+    else if (z_dtype == QLORA_DTYPE_F16) (void)run_bwd<QLORA_DTYPE_F16>(p, d_dtype, s);
+    else (void)run_bwd<QLORA_DTYPE_BF16>(p, d_dtype, s);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+}  // extern "C"

@@ -322,8 +322,56 @@ qlora_status qlora_dequantize_int8_absmax(const int8_t* codes, const float* alph
                                           void* out, int32_t out_dtype, void* stream);
 
 /*
+ * Distillation from a teacher's top logits: the loss that trains the adapters of
+ * a 4-bit student towards the answers of a 16-bit teacher (of another model or of
+ * this one before quantization), of which each row keeps its k largest logits.
+ * The pages have no counterpart; the gradient is the dY of qlora_linear_bwd /
+ * qlora_linear_bwd_adapters for the projection that gave the logits.
+ * Row m has the entries j with 0 <= i_j < V (any other index is no entry, and one
+ * at or above V raises the device BOUNDS flag); with the temperature T,
+ *     p_j  = softmax of t_j / T over the row's entries,
+ *     lse  = log sum_v exp(z_v / T) over the whole row,
+ *     loss = T^2 sum_j p_j (log p_j - z_{i_j} / T + lse).
+ * An index that comes twice is two entries of the same logit.  A row without
+ * entries, or whose teacher logits are all -inf, has loss 0.
+ *   logits          device [M, V] of z_dtype (any qlora_dtype), rows ld >= V elements
+ *                   apart; every row holds a finite logit.  -inf logits have probability 0.
+ *   teacher_idx     device int32 [M, k];  1 <= k <= 1024.
+ *   teacher_logits  device [M, k] of t_dtype (any qlora_dtype).
+ *   temperature     1e-3 .. 1e3.
+ *   loss, lse       device fp32 [M], written; the backward reads lse.
+ * Statistics and sums are fp32.  Deterministic.
+ * Errors: QLORA_ERR_INVALID_ARG (null pointer, dtype, k, temperature),
+ * QLORA_ERR_SHAPE (M < 1, V < 1 or above 2^31 - 1, ld < V, M * ld above 2^40),
+ * QLORA_ERR_ALIGN.
+ */
+qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,
+                                    const int32_t* teacher_idx, const void* teacher_logits, int32_t t_dtype, int32_t k,
+                                    float temperature, float* loss, float* lse, void* stream);
+
+/*
+ * Gradient of sum_m dloss[m] loss[m] with respect to the logits:
+ *     dz_v = dloss T (exp(z_v / T - lse) - sum_{j: i_j = v} p_j),  rounded once to d_dtype,
+ * and zeros in a row without entries or with dloss[m] = 0 (its logits are not read).
+ *   lse       device fp32 [M] from the forward with the same arguments.
+ *   dloss     device fp32 [M].
+ *   dlogits   device [M, V] of d_dtype (any qlora_dtype), rows ldd >= V elements apart;
+ *             columns V .. ldd-1 are left as they are.  It may be the logits' own
+ *             memory (same pointer, stride and element size); any other overlap is
+ *             QLORA_ERR_INVALID_ARG.
+ * Row strides that agree modulo 8 elements (equal ones do) take 16-byte accesses;
+ * others are read and written element by element.
+ * Other arguments and errors as qlora_distill_topk_fwd.
+ */
+qlora_status qlora_distill_topk_bwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,
+                                    const int32_t* teacher_idx, const void* teacher_logits, int32_t t_dtype, int32_t k,
+                                    float temperature, const float* lse, const float* dloss, void* dlogits,
+                                    int32_t d_dtype, int64_t ldd, void* stream);
+
+/*
  * Device error flags raised since the last clear (bit 0: a bounded wait timed
- * out; bit 1: a non-finite weight was seen).  Synchronizes the stream, reads
+ * out; bit 1: a non-finite weight was seen; bit 2: an index out of range was
+ * skipped).  Synchronizes the stream, reads
  * the flags of the current device and clears them when `clear` is nonzero.
  * Returns QLORA_ERR_TIMEOUT or QLORA_ERR_NONFINITE when a flag is set.
  */

@@ -1,0 +1,276 @@
+"""The distillation loss from a teacher's top logits and its gradient, against the formulas in fp64.
+
+Tolerances count roundings.  With Y the largest |z / T| log2(e) of a row, the exponent of an element
+is off by at most 3 Y 2^-24 (the constant, the reference and the fused multiply-add are each rounded),
+an exponential by 2^-22 more, and the sum of V of them by (V / 256 + 32) 2^-24 (each of 256 threads
+adds its share, a tree joins them).  E = (4 Y + V / 256 + 64) 2^-24 bounds the sum of these for lse
+and for log q; the teacher's side has the same bound with its own exponents.
+"""
+import math
+
+import pytest
+import torch
+
+import bit_nf4_quantized_23_b200 as q4
+from bit_nf4_quantized_23_b200 import _lib
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+E = {v: k for k, v in _lib.STATUS_NAMES.items()}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_nf4_quantized_23_b200.build import build
+    build()
+
+
+# ---------------------------------------------------------------------------- host
+
+FAKE = 0x7f0000000000      # never dereferenced: every call below fails validation first
+
+
+def test_refusals_on_the_host():
+    L = _lib.lib()
+    before = L.qlora_launch_count()
+
+    def fwd(z=FAKE, zt=0, ld=100, M=4, V=100, idx=FAKE, t=FAKE, tt=1, k=8, T=1.0, loss=FAKE, lse=FAKE):
+        return L.qlora_distill_topk_fwd(z, zt, ld, M, V, idx, t, tt, k, T, loss, lse, None)
+
+    def bwd(z=FAKE, zt=0, ld=104, M=4, V=100, idx=FAKE, t=FAKE, tt=1, k=8, T=1.0, lse=FAKE, dl=FAKE,
+            d=FAKE + (1 << 20), dt=0, ldd=104):
+        return L.qlora_distill_topk_bwd(z, zt, ld, M, V, idx, t, tt, k, T, lse, dl, d, dt, ldd, None)
+
+    for f in (fwd, bwd):
+        assert f(z=None) == E["QLORA_ERR_INVALID_ARG"]
+        assert f(z=FAKE + 2) == E["QLORA_ERR_ALIGN"]
+        assert f(idx=None) == E["QLORA_ERR_INVALID_ARG"]
+        assert f(t=FAKE + 4) == E["QLORA_ERR_ALIGN"]
+        assert f(lse=None) == E["QLORA_ERR_INVALID_ARG"]
+        assert f(zt=3) == f(tt=-1) == E["QLORA_ERR_INVALID_ARG"]
+        assert f(k=0) == f(k=1025) == E["QLORA_ERR_INVALID_ARG"]
+        for T in (0.0, -1.0, 1e-4, 1e4, float("nan"), float("inf")):
+            assert f(T=T) == E["QLORA_ERR_INVALID_ARG"]
+        assert f(M=0) == f(V=0) == f(ld=99) == f(V=1 << 31, ld=1 << 31) == f(ld=1 << 39) == E["QLORA_ERR_SHAPE"]
+    assert fwd(loss=None) == E["QLORA_ERR_INVALID_ARG"]
+    assert bwd(d=None) == bwd(dt=9) == bwd(dl=None) == E["QLORA_ERR_INVALID_ARG"]
+    assert bwd(ldd=99) == E["QLORA_ERR_SHAPE"]
+    # overlaps: another stride, another element size, a shifted start, the end of the logits
+    for bad in (dict(d=FAKE, ldd=112), dict(d=FAKE, dt=1), dict(d=FAKE + 16), dict(d=FAKE + 816)):
+        assert bwd(**bad) == E["QLORA_ERR_INVALID_ARG"]
+    assert L.qlora_launch_count() == before
+
+
+def test_binding_refuses_wrong_tensors():
+    z, i, t = torch.zeros(2, 8), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
+    with pytest.raises(ValueError):
+        q4.qlora_distill_topk_fwd(z, i, t)                       # not on a CUDA device
+    with pytest.raises(ValueError):
+        q4.qlora_distill_topk_fwd(z[0], i, t)
+    with pytest.raises(TypeError):
+        q4.qlora_distill_topk_fwd(z.double(), i, t)
+
+
+# ---------------------------------------------------------------------------- GPU
+
+
+def formulas(z, idx, t, T, dloss):
+    """(loss, lse, dz, sum_j p |log p - log q|) in fp64, row by row."""
+    z, t = z.double().cpu(), t.double().cpu()
+    idx, M, V = idx.cpu(), z.shape[0], z.shape[1]
+    loss, lse, dz, mag = torch.zeros(M).double(), torch.zeros(M).double(), torch.zeros(M, V).double(), torch.zeros(M).double()
+    for m in range(M):
+        y = z[m] / T
+        top = y[~y.isnan()].max()
+        lse[m] = top + (y - top).exp().sum().log()
+        ok = (idx[m] >= 0) & (idx[m] < V) & (t[m] > -math.inf)
+        if not ok.any():
+            continue
+        p = torch.softmax(t[m][ok] / T, 0)
+        i = idx[m][ok].long()
+        d = torch.where(p > 0, p.log() - (y[i] - lse[m]), torch.zeros(()).double())
+        loss[m] = T * T * (torch.where(p > 0, p * d, torch.zeros(()).double())).sum()
+        mag[m] = T * T * (p * d).abs().nan_to_num(0.0).sum()
+        if dloss[m] != 0:
+            dz[m] = (y - lse[m]).exp().index_add(0, i, -p) * T * dloss[m].double().cpu()
+    return loss, lse, dz, mag
+
+
+def unit(z, t, idx, T, V):
+    zf, tf = z.double().cpu(), t.double().cpu()
+    big = max(float(zf[zf.isfinite()].abs().max()), float(tf[tf.isfinite()].abs().max()))
+    return (4 * big / T * math.log2(math.e) + V / 256 + 64) * 2.0 ** -24
+
+
+def make(M, V, k, dt, tdt, seed, pad=0, std=2.5):
+    g = torch.Generator().manual_seed(seed)
+    z = (torch.randn(M, V + pad, generator=g) * std).to(dt)[:, :V].cuda() if pad else \
+        (torch.randn(M, V, generator=g) * std).to(dt).cuda()
+    if pad:
+        z = torch.nn.functional.pad(z, (0, pad), value=float("nan"))[:, :V]
+    idx = torch.randint(0, V, (M, k), generator=g).int()
+    idx[torch.rand(M, k, generator=g) < 0.2] = -1
+    t = (torch.randn(M, k, generator=g) * std).to(tdt)
+    dloss = torch.rand(M, generator=g) + 0.5
+    return z, idx.cuda(), t.cuda(), dloss.cuda()
+
+
+def check_case(z, idx, t, T, dloss, out_dtype, dlogits=None):
+    M, V = z.shape
+    ref_loss, ref_lse, ref_dz, mag = formulas(z, idx, t, T, dloss)
+    e = unit(z, t, idx, T, V)
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, T)
+    zc = z.double().cpu()
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, T, d_dtype=out_dtype, dlogits=dlogits)
+    torch.cuda.synchronize()
+    assert torch.all((lse.double().cpu() - ref_lse).abs() <= e * (1 + ref_lse.abs()))
+    assert torch.all((loss.double().cpu() - ref_loss).abs() <= 2 * e * (T * T + mag) + 2.0 ** -23 * ref_loss.abs())
+    # q and each p are off by their exponents' error; both times dloss T; then the rounding to the type
+    p_sum = ((zc / T - ref_lse[:, None]).exp() * T * dloss.double().cpu()[:, None] - ref_dz).abs()
+    q = (zc / T - ref_lse[:, None]).exp() * T * dloss.double().cpu()[:, None]
+    half = torch.finfo(out_dtype).eps / 2
+    # below the smallest normal number the step is constant: half of the smallest subnormal
+    tiny = torch.finfo(out_dtype).tiny * half + (1e-37 if out_dtype != torch.float16 else 0.0)
+    tol = 4 * e * (q + p_sum) + half * ref_dz.abs() + 2 * tiny
+    err = (dz.double().cpu() - ref_dz).abs()
+    assert dz.dtype == out_dtype
+    assert torch.all(err <= tol), float((err / tol).max())
+    return loss, lse, dz
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("fp16", "fp16"), ("fp32", "fp32"), ("fp32", "bf16"),
+                                    ("fp32", "fp16"), ("bf16", "fp32"), ("fp16", "bf16")])
+@pytest.mark.parametrize("M,V,k,T", [(1, 1, 1, 1.0), (3, 7, 2, 2.0), (5, 1000, 17, 1.0), (2, 33001, 64, 0.7),
+                                     (300, 4099, 33, 4.0)])
+def test_loss_and_gradient(dt, out, M, V, k, T):
+    z, idx, t, dloss = make(M, V, k, DT[dt], torch.float32, seed=M + V + k)
+    check_case(z, idx, t, T, dloss, DT[out])
+    assert q4.qlora_read_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tdt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("k", [1, 256, 257, 1024])
+def test_teacher_types_and_entry_counts(tdt, k):
+    z, idx, t, dloss = make(4, 5000, k, torch.bfloat16, DT[tdt], seed=k)
+    check_case(z, idx, t, 1.5, dloss, torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad,dpad", [(3, 3), (8, 0), (5, 0), (0, 7), (1, 9)])
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", "fp32"), ("bf16", "fp32")])
+def test_row_strides_and_columns_behind_the_row(pad, dpad, dt, out):
+    """Rows of a padded head: NaN behind the vocabulary is never read, and the padding of the gradient
+    keeps its values (equal strides, strides that agree modulo eight, and strides that do not)."""
+    M, V = 5, 1001
+    z, idx, t, dloss = make(M, V, 9, DT[dt], torch.float32, seed=11 + pad, pad=pad)
+    buf = torch.full((M, V + dpad), 7.0, dtype=DT[out], device="cuda")
+    check_case(z, idx, t, 1.0, dloss, DT[out], dlogits=buf[:, :V])
+    assert torch.all(buf[:, V:] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [9, 1001, 40000])
+def test_in_place_gradient_equals_the_separate_one(V):
+    z, idx, t, dloss = make(6, V, 8, torch.bfloat16, torch.float32, seed=V)
+    idx[0] = idx[0, 0].clamp(min=0)                              # one logit eight times
+    _, lse = q4.qlora_distill_topk_fwd(z, idx, t, 2.0)
+    apart = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, 2.0)
+    q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, 2.0, dlogits=z)
+    assert torch.equal(apart.view(torch.int16), z.view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [6, 400])
+def test_rows_without_entries_masks_and_repeated_indices(M):
+    V, k = 20011, 12
+    z, idx, t, dloss = make(M, V, k, torch.float32, torch.float32, seed=5)
+    idx[0] = -1                                                  # no entry
+    idx[1] = 777                                                 # the same index k times
+    t[2] = -math.inf                                             # every teacher logit masked
+    t[3] = torch.finfo(torch.float32).min                        # the lowest value: an even distribution
+    t[4, 1:] = -math.inf                                         # one entry left
+    dloss[5] = 0.0
+    z[0] = math.nan                                              # never read into a row without entries
+    z[2, 100] = math.inf
+    z[5, 3] = math.nan
+    z[1, :5000] = -math.inf                                      # masked vocabulary
+    z[4, 5000:] = torch.finfo(torch.float32).min
+    idx[4] = torch.arange(k, dtype=torch.int32, device="cuda")
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, 1.0)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, 1.0)
+    for m in (0, 2):
+        assert loss[m] == 0 and torch.all(dz[m] == 0)
+    assert torch.all(dz[5] == 0)
+    rows = [1, 3, 4] + list(range(6, M))
+    zr, ir, tr, dr = (v[rows].contiguous() for v in (z, idx, t, dloss))
+    zs = zr.clone()
+    zs[zs == torch.finfo(torch.float32).min] = -math.inf         # e^lowest is 0 as e^-inf is
+    tr64 = tr.clone()
+    tr64[tr64 == torch.finfo(torch.float32).min] = 0.0
+    ref_loss, ref_lse, ref_dz, mag = formulas(zs, ir, tr64, 1.0, dr)
+    e = unit(zs, tr64, ir, 1.0, V)
+    got = loss[rows].double().cpu()
+    # row 1: all of the teacher's weight on a masked logit, a loss of +inf on both sides
+    assert got[0] == math.inf and ref_loss[0] == math.inf
+    off = (got - ref_loss)[1:].abs()
+    assert torch.all(off <= (2 * e * (1 + mag) + 2.0 ** -23 * ref_loss.abs())[1:])
+    q = (zs.double().cpu() - ref_lse[:, None]).exp() * dr.double().cpu()[:, None]
+    tol = 4 * e * (q + (q - ref_dz).abs()) + 2.0 ** -24 * ref_dz.abs() + 1e-37
+    assert torch.all((dz[rows].double().cpu() - ref_dz).abs() <= tol)
+
+
+@pytest.mark.gpu
+def test_a_teacher_index_behind_the_vocabulary_is_flagged_and_skipped():
+    z, idx, t, dloss = make(3, 500, 4, torch.bfloat16, torch.float32, seed=9)
+    q4.qlora_read_device_errors(clear=True)
+    idx[1, 2] = 500
+    check_case(z, idx, t, 1.0, dloss, torch.float32)
+    assert q4.qlora_read_device_errors(clear=True) == 4
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences():
+    """(loss(z + h e) - loss(z - h e)) / 2h in fp64 of the formula agrees with the kernel's gradient."""
+    z, idx, t, _ = make(2, 50, 6, torch.float32, torch.float32, seed=3)
+    one = torch.ones(2, device="cuda")
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, 2.0)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, one, 2.0).double().cpu()
+    h = 1e-4
+    for v in (0, 17, int(idx[0][idx[0] >= 0][0]), 49):
+        up, down = z.double().cpu().clone(), z.double().cpu().clone()
+        up[:, v] += h
+        down[:, v] -= h
+        num = (formulas(up, idx, t, 2.0, one)[0] - formulas(down, idx, t, 2.0, one)[0]) / (2 * h)
+        # truncation h^2/6 of a third derivative below T^2 / T^3, cancellation 2^-52 |loss| / h, the kernel's own E
+        assert torch.all((num - dz[:, v]).abs() <= h * h + 1e-11 + 8 * unit(z, t, idx, 2.0, 50))
+
+
+@pytest.mark.gpu
+def test_capture_and_replay_on_a_side_stream_with_new_inputs():
+    s = torch.cuda.Stream()
+    a = make(7, 9001, 16, torch.bfloat16, torch.float32, seed=1)
+    b = make(7, 9001, 16, torch.bfloat16, torch.float32, seed=2)
+    z, idx, t, dloss = (v.clone() for v in a)
+    loss, lse = torch.empty(7, device="cuda"), torch.empty(7, device="cuda")
+    dz = torch.empty_like(z)
+
+    def step():
+        q4.qlora_distill_topk_fwd(z, idx, t, 1.0, loss=loss, lse=lse)
+        q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, 1.0, dlogits=dz)
+
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for src in (b, a):
+        for dst, v in zip((z, idx, t, dloss), src):
+            dst.copy_(v)
+        g.replay()
+        torch.cuda.synchronize()
+        want, want_lse = q4.qlora_distill_topk_fwd(*src[:3], 1.0)
+        assert torch.equal(loss, want) and torch.equal(lse, want_lse)
+        assert torch.equal(dz, q4.qlora_distill_topk_bwd(*src[:3], want_lse, src[3], 1.0))
