@@ -23,6 +23,7 @@ __all__ = [
     "qlora_quantize_nf4_dq",
     "qlora_quantize_nf4_dq_noalloc",
     "qlora_dequantize", "qlora_quantize_int8_absmax", "qlora_dequantize_int8_absmax", "qlora_merge_lora", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi", "qlora_linear_bwd",
+    "qlora_adapters_workspace_size", "qlora_linear_fwd_adapters", "qlora_linear_bwd_adapters",
     "qlora_distill_topk_fwd", "qlora_distill_topk_bwd",
     "qlora_read_device_errors", "qlora_selftest_bounded_wait", "qlora_launch_count", "qlora_timing_enable", "qlora_timing_read",
 ]
@@ -352,6 +353,86 @@ def _need_here(name: str, *tensors):
     for t in tensors:
         if t is not None and t.device.index != dev:
             raise ValueError(f"{name}: every tensor must be on the current CUDA device cuda:{dev}, got {t.device}")
+
+
+def qlora_adapters_workspace_size(M: int, N: int, K: int, r: int, n_adapters: int) -> int:
+    n = c_size_t()
+    check(lib().qlora_adapters_workspace_size(M, N, K, r, n_adapters, byref(n)), "qlora_adapters_workspace_size")
+    return n.value
+
+
+def _adapter_args(where, w, X, A_all, B_all, adapter_idx, scales, workspace):
+    """Checks of both directions; returns (M, n_adapters, r, workspace)."""
+    if A_all.dim() != 3:
+        raise ValueError("A_all must be 3-D [n_adapters, r, K]")
+    M, (n, r, _) = X.shape[0], A_all.shape
+    _need(X, w.compute_dtype, "X", (M, w.K))
+    _need(A_all, w.compute_dtype, "A_all", (n, r, w.K))
+    _need(B_all, w.compute_dtype, "B_all", (n, w.N, r))
+    _need(adapter_idx, torch.int32, "adapter_idx", (M,))
+    _need(scales, torch.float32, "scales", (n,))
+    if workspace is None:
+        workspace = torch.empty(qlora_adapters_workspace_size(M, w.N, w.K, r, n), dtype=torch.uint8, device=X.device)
+    _need_here(where, w.codes, X, A_all, B_all, adapter_idx, scales, workspace)
+    return M, n, r, workspace
+
+
+def qlora_linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor, B_all: torch.Tensor,
+                              adapter_idx: torch.Tensor, scales: torch.Tensor, y_dtype=None, save_U: bool = True,
+                              out: torch.Tensor | None = None, U_out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, stream=None):
+    """The adapters of many requests over one base, any number of tokens: Y[m] = X[m] W_hat^T +
+    s_a (X[m] A_a^T) B_a^T with a = adapter_idx[m] (negative: base only) and s_a = scales[a].
+    A_all [n, r, K] and B_all [n, N, r] in the compute dtype (smaller ranks zero-padded to r),
+    adapter_idx int32 [M], scales fp32 [n], all on the device.  Returns (Y, U) with U fp32 [M, r]
+    (or None)."""
+    M, n, r, workspace = _adapter_args("qlora_linear_fwd_adapters", w, X, A_all, B_all, adapter_idx, scales, workspace)
+    y_dtype = w.compute_dtype if y_dtype is None else y_dtype
+    if out is None:
+        out = torch.empty(M, w.N, dtype=y_dtype, device=X.device)
+    _need(out, y_dtype, "Y", (M, w.N))
+    if save_U and U_out is None:
+        U_out = torch.empty(M, r, dtype=torch.float32, device=X.device)
+    if U_out is not None:
+        _need(U_out, torch.float32, "U", (M, r))
+    _need_here("qlora_linear_fwd_adapters", out, U_out)
+    ws = w.c_struct()
+    check(lib().qlora_linear_fwd_adapters(byref(ws), _ptr(X), M, _ptr(A_all), _ptr(B_all), n, _ptr(adapter_idx), r,
+                                          _ptr(scales), _ptr(out), _dtype_code(y_dtype), _ptr(U_out),
+                                          _ptr(workspace), workspace.numel(), _stream(stream)),
+          "qlora_linear_fwd_adapters")
+    return out, U_out
+
+
+def qlora_linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A_all: torch.Tensor,
+                              B_all: torch.Tensor, adapter_idx: torch.Tensor, scales: torch.Tensor,
+                              U_saved: torch.Tensor | None = None, need_dX: bool = True, dx_dtype=None,
+                              dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                              dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dX, dA_all, dB_all) of <dY, Y> of qlora_linear_fwd_adapters: dA_all fp32 [n, r, K] and dB_all
+    fp32 [n, N, r] hold every adapter's gradient over its own tokens.  dX is None when need_dX is False."""
+    M, n, r, workspace = _adapter_args("qlora_linear_bwd_adapters", w, X, A_all, B_all, adapter_idx, scales, workspace)
+    dx_dtype = w.compute_dtype if dx_dtype is None else dx_dtype
+    _need(dY, w.compute_dtype, "dY", (M, w.N))
+    if U_saved is not None:
+        _need(U_saved, torch.float32, "U_saved", (M, r))
+    if need_dX and dX is None:
+        dX = torch.empty(M, w.K, dtype=dx_dtype, device=X.device)
+    if dX is not None:
+        _need(dX, dx_dtype, "dX", (M, w.K))
+    if dA is None:
+        dA = torch.empty(n, r, w.K, dtype=torch.float32, device=X.device)
+    if dB is None:
+        dB = torch.empty(n, w.N, r, dtype=torch.float32, device=X.device)
+    _need(dA, torch.float32, "dA", (n, r, w.K))
+    _need(dB, torch.float32, "dB", (n, w.N, r))
+    _need_here("qlora_linear_bwd_adapters", dY, U_saved, dX, dA, dB)
+    ws = w.c_struct()
+    check(lib().qlora_linear_bwd_adapters(byref(ws), _ptr(X), _ptr(dY), M, _ptr(A_all), _ptr(B_all), n,
+                                          _ptr(adapter_idx), r, _ptr(scales), _ptr(U_saved), _ptr(dX),
+                                          _dtype_code(dx_dtype), _ptr(dA), _ptr(dB), _ptr(workspace),
+                                          workspace.numel(), _stream(stream)), "qlora_linear_bwd_adapters")
+    return dX, dA, dB
 
 
 def _rows(t: torch.Tensor, name: str, shape=None):

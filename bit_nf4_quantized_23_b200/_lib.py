@@ -56,6 +56,12 @@ SIGNATURES = {
     "qlora_linear_bwd": (c_int32, [_W, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_float,
                                    c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
                                    c_void_p]),
+    "qlora_linear_fwd_adapters": (c_int32, [_W, c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_void_p, c_int32,
+                                            c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qlora_linear_bwd_adapters": (c_int32, [_W, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_void_p,
+                                            c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                                            c_void_p, c_size_t, c_void_p]),
+    "qlora_adapters_workspace_size": (c_int32, [c_int64, c_int64, c_int64, c_int32, c_int32, POINTER(c_size_t)]),
     "qlora_distill_topk_fwd": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int32,
                                          c_int32, c_float, c_void_p, c_void_p, c_void_p]),
     "qlora_distill_topk_bwd": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int32,

@@ -1,0 +1,1003 @@
+// The linear layer with one adapter per token: the low-rank adapters of many requests at once
+// beside the shared quantized projection, forward and backward ("Ch.09 QLoRA 与量化", section
+// "3. 一个底座，多个适配器": one shared compressed base, one thin adapter per task).
+//
+// With a = adapter_idx[m] (none: a = -1) and s_a = scales[a]:
+//     U[m]  = X[m] A_a^T                     Y[m]  = X[m] W_hat^T + s_a U[m] B_a^T
+//     dU[m] = s_a dY[m] B_a                  dX[m] = dY[m] W_hat + dU[m] A_a
+//     dA_a  = sum over its tokens of dU[m]^T X[m]
+//     dB_a  = sum over its tokens of s_a dY[m]^T U[m]
+//
+// Tokens stay where they are: nothing is sorted or gathered.  Lists built on the device say which
+// adapters occur in which token tile and in which of its rows, and
+//   - products whose rows are tokens (U, dU here; Y and dX in gemm_tc.cu) run one pass per adapter of
+//     the tile, whose MMAs write only that adapter's rows (the output-lane mask of tcgen05.mma);
+//   - products that sum over tokens (dA, dB) run over the adapter's own token tiles, and a tile that
+//     it shares has the other tokens' rows zeroed in shared memory first, so that Inf or NaN in one
+//     request's activations stays out of another's gradient.
+// A tile of contiguous requests meets few adapters, so the passes cost little; any order of tokens is
+// correct.
+#include <climits>
+#include <algorithm>
+
+#include "gemm_tc.cuh"
+#include "qlora_internal.cuh"
+#include "tc_ptx.cuh"
+#include "timing.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kPartTile = 128;                    // token rows of a U / dU tile
+constexpr int kPartEntry = 8;                     // words: row mask [4], adapter, 3 unused
+constexpr int kGradTile = 64;                     // tokens of one reduction step of dA / dB
+constexpr uint32_t kStage16K = 128 * 128;
+constexpr uint32_t kMaxSmem = 227 * 1024;
+
+// ---------------------------------------------------------------------------- lists
+
+// What the kernels below read of adapter_idx; all pieces live in the caller's workspace.
+struct AdapterLists {
+    int32_t* tok;             // [M] adapter of each token, -1 for none or an index out of range
+    uint32_t* n512;           // [tiles of 512] entries of the tile
+    uint32_t* e512;           // [tiles of 512][cap512][kAdEntry]
+    uint32_t* n128;           // [tiles of 128]
+    uint32_t* e128;           // [tiles of 128][cap128][kPartEntry]
+    uint32_t* n_grad;         // [n_adapters] token tiles of 64 that hold the adapter
+    uint4* e_grad;            // [n_adapters][tiles of 64]: tile, row mask (2 words), 1 if no other rows
+    int32_t cap512, cap128;
+    int32_t tiles64;
+};
+
+// Block b < tiles512: the lists of tokens 512 b .. 512 b + 511, one thread per token.  The first token
+// of a tile with an adapter opens its entry (entries in order of first appearance, so the lists do not
+// depend on timing), and each warp's tokens of one adapter write one word of its mask.
+// Block tiles512 + a: the token tiles of adapter a.
+__global__ void __launch_bounds__(512)
+build_lists(const int32_t* __restrict__ idx, int64_t M, int32_t n_adapters, int64_t tiles512, AdapterLists l,
+            uint32_t* err) {
+    grid_dependency_wait();
+    allow_dependents();
+    __shared__ __align__(16) int32_t ids[512];
+    __shared__ int32_t slot[512];
+    __shared__ uint32_t ballots[16];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (blockIdx.x >= tiles512) {
+        const int32_t a = (int32_t)(blockIdx.x - tiles512);
+        uint4* out = l.e_grad + (int64_t)a * l.tiles64;
+        int32_t found = 0;
+        for (int64_t m0 = 0; m0 < M; m0 += 512) {
+            const int64_t m = m0 + t;
+            const uint32_t mine = __ballot_sync(0xffffffffu, m < M && idx[m] == a);
+            if (lane == 0) ballots[warp] = mine;
+            __syncthreads();
+            int32_t before = 0, total = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const bool any = (ballots[2 * q] | ballots[2 * q + 1]) != 0;
+                before += any && q < t;
+                total += any;
+            }
+            if (t < 8 && (ballots[2 * t] | ballots[2 * t + 1]) != 0) {
+                const int64_t left = M - (m0 + 64 * t);       // rows of this token tile
+                const uint32_t lo = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+                const uint32_t hi = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1u : 0u;
+                const uint32_t b0 = ballots[2 * t], b1 = ballots[2 * t + 1];
+                out[found + before] = make_uint4((uint32_t)(m0 / 64 + t), b0, b1, (b0 == lo && b1 == hi) ? 1u : 0u);
+            }
+            found += total;
+            __syncthreads();
+        }
+        if (t == 0) l.n_grad[a] = (uint32_t)found;
+        return;
+    }
+    const int64_t m = (int64_t)blockIdx.x * 512 + t;
+    int32_t a = m < M ? idx[m] : -1;
+    if (a >= n_adapters) {
+        atomicOr(err, ERR_FLAG_BOUNDS);
+        a = -1;
+    }
+    if (a < 0) a = -1;
+    if (m < M) l.tok[m] = a;
+    ids[t] = a;
+    __syncthreads();
+    int f512 = t, f128 = t;                                   // first token of the tile with this adapter
+    const int sub = t & ~127;
+    for (int j = 508; j >= 0; j -= 4) {
+        const int4 v = *reinterpret_cast<const int4*>(ids + j);
+        const int j0 = v.x == a ? j : v.y == a ? j + 1 : v.z == a ? j + 2 : v.w == a ? j + 3 : 512;
+        if (j0 < f512) f512 = j0;
+        if (j0 >= sub && j0 < f128) f128 = j0;
+    }
+    const uint32_t same = __match_any_sync(0xffffffffu, a);
+    const bool writes = a >= 0 && lane == __ffs((int)same) - 1;
+
+    // tiles of 512
+    bool first = a >= 0 && f512 == t;
+    uint32_t b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) ballots[warp] = b;
+    __syncthreads();
+    int before = __popc(b & ((1u << lane) - 1u)), total = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        const int c = __popc(ballots[w]);
+        if (w < warp) before += c;
+        total += c;
+    }
+    uint32_t* e512 = l.e512 + (int64_t)blockIdx.x * l.cap512 * kAdEntry;
+    if (t == 0) l.n512[blockIdx.x] = (uint32_t)total;
+    if (first) {
+        slot[t] = before;
+        uint4* e = reinterpret_cast<uint4*>(e512 + (int64_t)before * kAdEntry);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e[q] = make_uint4(0, 0, 0, 0);
+        e[4] = make_uint4((uint32_t)a, 0, 0, 0);
+    }
+    __syncthreads();
+    if (writes) e512[slot[f512] * kAdEntry + warp] = same;
+    __syncthreads();
+
+    // tiles of 128
+    first = a >= 0 && f128 == t;
+    b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) ballots[warp] = b;
+    __syncthreads();
+    before = __popc(b & ((1u << lane) - 1u));
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int c = __popc(ballots[(warp & ~3) + w]);
+        if (w < (warp & 3)) before += c;
+        total += c;
+    }
+    const int64_t tile128 = (int64_t)blockIdx.x * 4 + (t >> 7);
+    if (tile128 * 128 < M) {
+        uint32_t* e128 = l.e128 + tile128 * l.cap128 * kPartEntry;
+        if ((t & 127) == 0) l.n128[tile128] = (uint32_t)total;
+        if (first) {
+            slot[t] = before;
+            uint4* e = reinterpret_cast<uint4*>(e128 + (int64_t)before * kPartEntry);
+            e[0] = make_uint4(0, 0, 0, 0);
+            e[1] = make_uint4((uint32_t)a, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    if (writes && tile128 * 128 < M) l.e128[(tile128 * l.cap128 + slot[f128]) * kPartEntry + (warp & 3)] = same;
+}
+
+// ---------------------------------------------------------------------------- U and dU
+
+// partial[split][m][0 .. Rn) = sum over the split's 64-wide reduction steps of S[m] . V_a[j], S = X
+// with V = A_all (reduction over K), or S = dY with V = B_all (reduction over N, V MN-major).
+// CTA (token tile of 128, split): each reduction step loads the S tile once and one tile of V for each
+// adapter of the tile; the adapter's MMA writes its own rows of the one accumulator.  Rows without an
+// adapter are written as zeros.  Two rings, so that one S tile serves many V tiles.
+// Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 epilogue.
+constexpr int kPartThreads = 192;
+
+struct PartParams {
+    int64_t M;
+    int32_t Rn;               // ranks rounded up to 16: columns of the accumulator
+    int32_t ksteps_total, ksteps_per_split;
+    uint32_t tmem_cols, s_stages, v_stages, v_tile;
+    int32_t f16;
+    const uint32_t* count;
+    const uint32_t* entry;
+    int32_t cap;
+    const int32_t* tok;
+    float* partial;
+    uint32_t* err;
+};
+
+struct PartLayout {
+    uint32_t off_v, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
+};
+__host__ __device__ inline PartLayout part_layout(uint32_t s_stages, uint32_t v_stages, uint32_t v_tile) {
+    PartLayout l;
+    l.off_v = s_stages * kStage16K;
+    l.off_mask = l.off_v + v_stages * v_tile;
+    l.off_adapter = l.off_mask + 128 * 16;
+    l.off_bars = l.off_adapter + 128 * 4;
+    l.off_slot = l.off_bars + (2 * s_stages + 2 * v_stages + 1) * 8;
+    l.off_abort = l.off_slot + 4;
+    l.alloc = l.off_abort + 4 + 1024;
+    return l;
+}
+
+template <bool V_MN>
+__global__ void __launch_bounds__(kPartThreads, 2)
+tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmV, PartParams p) {
+    grid_dependency_wait();
+    allow_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - ptx::smem_addr(smem_raw));
+    const PartLayout lay = part_layout(p.s_stages, p.v_stages, p.v_tile);
+    const int SS = (int)p.s_stages, VS = (int)p.v_stages;
+    const uint32_t sS = base, sV = base + lay.off_v;
+    const uint32_t bar_sfull = base + lay.off_bars, bar_sempty = bar_sfull + 8 * SS;
+    const uint32_t bar_vfull = bar_sempty + 8 * SS, bar_vempty = bar_vfull + 8 * VS;
+    const uint32_t bar_acc = bar_vempty + 8 * VS;
+    uint4* mask = reinterpret_cast<uint4*>(gbase + lay.off_mask);
+    int32_t* adapter = reinterpret_cast<int32_t*>(gbase + lay.off_adapter);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + lay.off_slot);
+    volatile int* abort = reinterpret_cast<volatile int*>(gbase + lay.off_abort);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row0 = (int64_t)blockIdx.x * kPartTile;
+    const int k_begin = blockIdx.y * p.ksteps_per_split;
+    const int k_end = min(p.ksteps_total, k_begin + p.ksteps_per_split);
+    const int n_ad = (int)p.count[blockIdx.x];
+    const int nk = n_ad > 0 ? k_end - k_begin : 0;
+
+    if (threadIdx.x < n_ad) {
+        const uint32_t* e = p.entry + ((int64_t)blockIdx.x * p.cap + threadIdx.x) * kPartEntry;
+        const uint4 v = *reinterpret_cast<const uint4*>(e);
+        mask[threadIdx.x] = make_uint4(~v.x, ~v.y, ~v.z, ~v.w);
+        adapter[threadIdx.x] = (int32_t)e[4];
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SS; ++s) {
+            ptx::mbar_init(bar_sfull + 8 * s, 1);
+            ptx::mbar_init(bar_sempty + 8 * s, 1);
+        }
+        for (int s = 0; s < VS; ++s) {
+            ptx::mbar_init(bar_vfull + 8 * s, 1);
+            ptx::mbar_init(bar_vempty + 8 * s, 1);
+        }
+        ptx::mbar_init(bar_acc, 1);
+        *abort = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+        ptx::tma_prefetch_map(&tmS);
+        ptx::tma_prefetch_map(&tmV);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(base + lay.off_slot, p.tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        int s = 0, v = 0, s_issued = 0, v_issued = 0;
+        uint32_t s_ph = 0, v_ph = 0;
+        bool ok = true;
+        for (int i = 0; i < nk && ok; ++i) {
+            const int ks = k_begin + i;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_sempty + 8 * s, s_ph ^ 1u, abort, p.err));
+            if (!ok) break;
+            if (ptx::elect_one_sync()) {
+                ptx::mbar_arrive_expect_tx(bar_sfull + 8 * s, kStage16K);
+                ptx::tma_load_2d(sS + s * kStage16K, &tmS, ks * 64, (int32_t)row0, bar_sfull + 8 * s);
+            }
+            __syncwarp();
+            ++s_issued;
+            if (++s == SS) { s = 0; s_ph ^= 1u; }
+            for (int e = 0; e < n_ad; ++e) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_vempty + 8 * v, v_ph ^ 1u, abort, p.err));
+                if (!ok) break;
+                if (ptx::elect_one_sync()) {
+                    const uint32_t fb = bar_vfull + 8 * v, dst = sV + v * p.v_tile;
+                    ptx::mbar_arrive_expect_tx(fb, p.v_tile);
+                    if (!V_MN) {
+                        ptx::tma_load_3d(dst, &tmV, ks * 64, 0, adapter[e], fb);
+                    } else {
+                        for (uint32_t c = 0; c * 8192u < p.v_tile; ++c)
+                            ptx::tma_load_3d(dst + c * 8192u, &tmV, (int32_t)c * 64, ks * 64, adapter[e], fb);
+                    }
+                }
+                __syncwarp();
+                ++v_issued;
+                if (++v == VS) { v = 0; v_ph ^= 1u; }
+            }
+        }
+        if (*abort) {   // drain this CTA's copies in flight before it exits
+            for (int c = max(0, s_issued - SS); c < s_issued; ++c)
+                ptx::mbar_wait_drain(bar_sfull + 8 * (c % SS), (uint32_t)(c / SS) & 1u);
+            for (int c = max(0, v_issued - VS); c < v_issued; ++c)
+                ptx::mbar_wait_drain(bar_vfull + 8 * (c % VS), (uint32_t)(c / VS) & 1u);
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, p.Rn, 0, V_MN ? 1 : 0), p.f16 != 0);
+        int s = 0, v = 0;
+        uint32_t s_ph = 0, v_ph = 0;
+        bool ok = true;
+        for (int i = 0; i < nk && ok; ++i) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_sfull + 8 * s, s_ph, abort, p.err));
+            for (int e = 0; e < n_ad && ok; ++e) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_vfull + 8 * v, v_ph, abort, p.err));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint4 mk = mask[e];
+                const uint32_t off[4] = {mk.x, mk.y, mk.z, mk.w};
+                if (ptx::elect_one_sync()) {
+                    const uint32_t a_base = sS + s * kStage16K, b_base = sV + v * p.v_tile;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_bf16_ss_lanes(tmem, ptx::smem_desc_sw128(a_base + kk * 32, 16, 1024),
+                                               V_MN ? ptx::smem_desc_sw128(b_base + kk * 2048, 8192, 1024)
+                                                    : ptx::smem_desc_sw128(b_base + kk * 32, 16, 1024),
+                                               idesc, (i | kk) != 0 ? 1u : 0u, off);
+                    ptx::mma_commit(bar_vempty + 8 * v);
+                    if (e == n_ad - 1) ptx::mma_commit(bar_sempty + 8 * s);
+                }
+                __syncwarp();
+                if (++v == VS) { v = 0; v_ph ^= 1u; }
+            }
+            if (++s == SS) { s = 0; s_ph ^= 1u; }
+        }
+        if (ptx::elect_one_sync()) {
+            ptx::mma_commit(bar_acc);
+            if (*abort) ptx::mbar_wait_drain(bar_acc, 0);   // issued MMAs finish before TMEM is freed
+        }
+        __syncwarp();
+    } else {
+        const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
+        ptx::tc_fence_after();
+        if (acc_ok) {
+            const uint32_t quad = (uint32_t)(warp & 3);
+            const int64_t row = row0 + quad * 32 + lane;
+            const bool have = row < p.M && nk > 0 && p.tok[row] >= 0;
+            float* dst = p.partial + ((int64_t)blockIdx.y * p.M + row) * p.Rn;
+#pragma unroll 1
+            for (int c = 0; c < p.Rn / 16; ++c) {
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + c * 16, v);
+                ptx::tmem_ld_wait();
+                if (row < p.M) {
+                    uint4* d4 = reinterpret_cast<uint4*>(dst + c * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        d4[i] = have ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, p.tmem_cols);
+    }
+}
+
+// V[m, j] = the sum of the splits' partials, in split order (out, fp32 [M, r]; may be null), and the
+// hi/lo halves of s_a V[m, j] in the 16-bit compute type (V2 [M, 2R], zeros for j >= r and for tokens
+// without an adapter; may be null).  hi = t(v), lo = t(v - hi): together within 2^-17 of v in bf16.
+// With splits = 0 the values come from V itself (a saved U).
+__global__ void __launch_bounds__(256)
+finish_part(const float* __restrict__ partial, int splits, int64_t M, int r, int Rn, int R,
+            const int32_t* __restrict__ tok, const float* __restrict__ scales, float* __restrict__ out,
+            uint16_t* __restrict__ V2, bool f16) {
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M * R) return;
+    const int64_t m = i / R;
+    const int j = (int)(i - m * R);
+    const int32_t a = tok[m];
+    float v = 0.f;
+    if (j < r && a >= 0) {
+        if (splits == 0) {
+            v = partial[m * r + j];
+        } else {
+            const int64_t stride = M * Rn;
+            const float* q = partial + m * Rn + j;
+            int s = 0;
+            for (; s + 8 <= splits; s += 8) {
+                float w[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) w[u] = q[(s + u) * stride];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v = __fadd_rn(v, w[u]);
+            }
+            for (; s < splits; ++s) v = __fadd_rn(v, q[s * stride]);
+        }
+    }
+    if (out && j < r) out[m * r + j] = v;
+    if (V2) {
+        const float sv = (j < r && a >= 0) ? __fmul_rn(scales[a], v) : 0.f;
+        const uint32_t hi = to16_rn(sv, f16);
+        V2[m * 2 * R + j] = (uint16_t)hi;
+        V2[m * 2 * R + R + j] = (uint16_t)to16_rn(__fsub_rn(sv, from16(hi, f16)), f16);
+    }
+}
+
+// ---------------------------------------------------------------------------- dA and dB
+
+// dA_a^T[k, j] = sum over the adapter's tokens of X[m, k] dU[m, j], and dB_a[n, j] likewise of dY and
+// s_a U, in one launch: CTA (x, a) computes 128 rows k (or n) of adapter a over the adapter's token
+// tiles.  Operand A is the [64 tokens x 128] tile of X or dY (MN-major), operand B the hi and lo halves
+// of dU or s U side by side (one MMA of N = 2R, the two halves added in fp32 in the epilogue) or, for
+// R > 128, one after the other into the same accumulator.
+// Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 zero the rows of other
+// tokens in tiles that the adapter shares, then run the epilogue.
+constexpr int kGradThreads = 192;
+
+struct GradParams {
+    int64_t M, K, N;
+    int32_t r, R;
+    int32_t tiles_k;          // CTAs x < tiles_k compute dA, the others dB
+    uint32_t stages, v_bytes, tmem_cols;
+    int32_t f16;
+    const uint32_t* n_grad;
+    const uint4* e_grad;
+    int32_t tiles64;
+    float* dA;                // [n, r, K]
+    float* dB;                // [n, N, r]
+    uint32_t* err;
+};
+
+struct GradLayout {
+    uint32_t off_v, off_bars, off_slot, off_abort, alloc;
+};
+__host__ __device__ inline GradLayout grad_layout(uint32_t stages, uint32_t v_bytes) {
+    GradLayout l;
+    l.off_v = stages * kStage16K;
+    l.off_bars = l.off_v + stages * v_bytes;
+    l.off_slot = l.off_bars + (3 * stages + 1) * 8;
+    l.off_abort = l.off_slot + 4;
+    l.alloc = l.off_abort + 4 + 1024;
+    return l;
+}
+
+__global__ void __launch_bounds__(kGradThreads, 2)
+tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmdY,
+                 const __grid_constant__ CUtensorMap tmdU2, const __grid_constant__ CUtensorMap tmU2, GradParams p) {
+    grid_dependency_wait();
+    allow_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - ptx::smem_addr(smem_raw));
+    const GradLayout lay = grad_layout(p.stages, p.v_bytes);
+    const int S = (int)p.stages;
+    const uint32_t sS = base, sV = base + lay.off_v;
+    const uint32_t bar_full = base + lay.off_bars, bar_ready = bar_full + 8 * S, bar_empty = bar_ready + 8 * S;
+    const uint32_t bar_acc = bar_empty + 8 * S;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + lay.off_slot);
+    volatile int* abort = reinterpret_cast<volatile int*>(gbase + lay.off_abort);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool is_a = (int)blockIdx.x < p.tiles_k;
+    const int64_t row0 = (int64_t)(is_a ? blockIdx.x : blockIdx.x - p.tiles_k) * 128;
+    const int32_t ad = (int32_t)blockIdx.y;
+    const int nt = (int)p.n_grad[ad];
+    const uint4* list = p.e_grad + (int64_t)ad * p.tiles64;
+    const int chunks = (int)(p.v_bytes / 8192);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_ready + 8 * s, 4);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        ptx::mbar_init(bar_acc, 1);
+        *abort = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(base + lay.off_slot, p.tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        int32_t tile = nt > 0 ? (int32_t)__ldg(&list[0].x) : 0;
+        for (int i = 0; i < nt; ++i) {
+            const int32_t next = i + 1 < nt ? (int32_t)__ldg(&list[i + 1].x) : 0;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * s, ph ^ 1u, abort, p.err))) break;
+            issued = i + 1;
+            if (ptx::elect_one_sync()) {
+                const uint32_t fb = bar_full + 8 * s, s_dst = sS + s * kStage16K, v_dst = sV + s * p.v_bytes;
+                const CUtensorMap* ms = is_a ? &tmX : &tmdY;
+                const CUtensorMap* mv = is_a ? &tmdU2 : &tmU2;
+                ptx::mbar_arrive_expect_tx(fb, kStage16K + p.v_bytes);
+                ptx::tma_load_2d(s_dst, ms, (int32_t)row0, tile * kGradTile, fb);
+                ptx::tma_load_2d(s_dst + 8192, ms, (int32_t)row0 + 64, tile * kGradTile, fb);
+                for (int c = 0; c < chunks; ++c) ptx::tma_load_2d(v_dst + c * 8192, mv, c * 64, tile * kGradTile, fb);
+            }
+            __syncwarp();
+            tile = next;
+            if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        if (*abort) {   // drain this CTA's copies in flight before it exits
+            for (int i = max(0, issued - S); i < issued; ++i)
+                ptx::mbar_wait_drain(bar_full + 8 * (i % S), (uint32_t)(i / S) & 1u);
+        }
+    } else if (warp == 1) {
+        const bool side = p.R <= 128;                         // hi and lo side by side in one MMA
+        const uint32_t idesc =
+            ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, side ? 2 * p.R : p.R, 1, 1), p.f16 != 0);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int i = 0; i < nt && ok; ++i) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_ready + 8 * s, ph, abort, p.err));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one_sync()) {
+                const uint32_t a_base = sS + s * kStage16K, b_base = sV + s * p.v_bytes;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint64_t ad_desc = ptx::smem_desc_sw128(a_base + kk * 2048, 8192, 1024);
+                    ptx::mma_bf16_ss(tmem, ad_desc, ptx::smem_desc_sw128(b_base + kk * 2048, 8192, 1024), idesc,
+                                     (i | kk) != 0 ? 1u : 0u);
+                    if (!side)
+                        ptx::mma_bf16_ss(tmem, ad_desc,
+                                         ptx::smem_desc_sw128(b_base + (p.R / 64) * 8192 + kk * 2048, 8192, 1024), idesc, 1u);
+                }
+                ptx::mma_commit(bar_empty + 8 * s);
+            }
+            __syncwarp();
+            if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        if (ptx::elect_one_sync()) {
+            ptx::mma_commit(bar_acc);
+            if (*abort) ptx::mbar_wait_drain(bar_acc, 0);   // issued MMAs finish before TMEM is freed
+        }
+        __syncwarp();
+    } else {
+        const int t = threadIdx.x - 64, row = t & 63, half = t >> 6;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        uint4 e = nt > 0 ? __ldg(list) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < nt && ok; ++i) {
+            const uint4 next = i + 1 < nt ? __ldg(list + i + 1) : make_uint4(0, 0, 0, 0);
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * s, ph, abort, p.err));
+            if (!ok) break;
+            if (e.w == 0u) {
+                const bool mine = ((row < 32 ? e.y : e.z) >> (row & 31)) & 1u;
+                if (!mine) {   // a token is one 128-byte row of every image
+                    const uint32_t x = sS + s * kStage16K + half * 8192u + row * 128u;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(x + 16 * c), "r"(0) : "memory");
+                    for (int q = half; q < chunks; q += 2) {
+                        const uint32_t v = sV + s * p.v_bytes + q * 8192u + row * 128u;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v + 16 * c), "r"(0) : "memory");
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * s);
+            e = next;
+            if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
+        ptx::tc_fence_after();
+        if (acc_ok) {
+            const uint32_t quad = (uint32_t)(warp & 3);
+            const int64_t orow = row0 + quad * 32 + lane;
+            const bool in = orow < (is_a ? p.K : p.N);
+            float* dst = is_a ? p.dA + (int64_t)ad * p.r * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r;
+            const bool vec = !is_a && p.r % 4 == 0;
+#pragma unroll 1
+            for (int c = 0; c * 16 < p.r; ++c) {
+                float v[16];
+                if (nt > 0) {
+                    uint32_t hi[16], lo[16];
+                    ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + c * 16, hi);
+                    if (p.R <= 128) ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + p.R + c * 16, lo);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = p.R <= 128 ? __fadd_rn(__uint_as_float(hi[q]), __uint_as_float(lo[q])) : __uint_as_float(hi[q]);
+                } else {                                      // no token has this adapter
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] = 0.f;
+                }
+                if (!in) continue;
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const int j = c * 16 + q;
+                    if (vec) {
+                        if (j < p.r) *reinterpret_cast<float4*>(dst + j) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (j + u < p.r) dst[is_a ? (int64_t)(j + u) * p.K : j + u] = v[q + u];
+                    }
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, p.tmem_cols);
+    }
+}
+
+// out[i, 0 .. cols_out) = in[i, 0 .. cols) and zeros: 16-bit rows brought to a multiple of 16 bytes,
+// which TMA needs of its row strides (B_all with r % 8 != 0, dY with N % 8 != 0).
+__global__ void __launch_bounds__(256)
+pad_rows(const uint16_t* __restrict__ in, int64_t rows, int64_t cols, int64_t cols_out, uint4* __restrict__ out) {
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t chunks = cols_out / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * chunks) return;
+    const int64_t row = i / chunks, c = (i - row * chunks) * 8;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t j = c + 2 * q;
+        const uint32_t lo = j < cols ? in[row * cols + j] : 0u, hi = j + 1 < cols ? in[row * cols + j + 1] : 0u;
+        w[q] = lo | (hi << 16);
+    }
+    out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------- host
+
+inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Half width of the hi/lo operands: 32 (both halves share one 64-wide step) or a multiple of 64.
+inline int32_t half_width(int32_t r) { return r <= 32 ? 32 : (int32_t)round_up(r, 64); }
+
+// Workspace, every piece 256-byte aligned:
+//   the lists; U, fp32 [M, r] (when the caller keeps none); U2 and dU2, 16-bit [M, 2R] (hi | lo of s U
+//   and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
+//   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
+struct AdaptersWs {
+    size_t tok, n512, e512, n128, e128, n_grad, e_grad, u, u2, du2, part, b8, dy8, total;
+    int32_t cap512, cap128, tiles64;
+    int64_t tiles512;
+};
+
+int part_splits(int64_t M, int64_t red, int32_t r) { return lora_splits(M, (int)((red + 63) / 64), (int)round_up(r, 64), false); }
+
+AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
+    AdaptersWs w;
+    const int64_t R = half_width(r), Rn = round_up(r, 16), t128 = (M + 127) / 128;
+    w.tiles512 = (M + kAdTile - 1) / kAdTile;
+    w.cap512 = (int32_t)std::min<int64_t>({(int64_t)kAdTile, n, M});
+    w.cap128 = (int32_t)std::min<int64_t>({(int64_t)kPartTile, n, M});
+    w.tiles64 = (int32_t)((M + 63) / 64);
+    size_t o = 0;
+    auto piece = [&o](size_t bytes) { const size_t at = o; o += align_up(bytes, 256); return at; };
+    w.tok = piece(M * 4);
+    w.n512 = piece(w.tiles512 * 4);
+    w.e512 = piece((size_t)w.tiles512 * w.cap512 * kAdEntry * 4);
+    w.n128 = piece(t128 * 4);
+    w.e128 = piece((size_t)t128 * w.cap128 * kPartEntry * 4);
+    w.n_grad = piece(n * 4);
+    w.e_grad = piece((size_t)n * w.tiles64 * 16);
+    w.u = piece((size_t)M * r * 4);
+    w.u2 = piece((size_t)M * 2 * R * 2);
+    w.du2 = piece((size_t)M * 2 * R * 2);
+    size_t part = (size_t)std::max(part_splits(M, K, r), part_splits(M, N, r)) * M * Rn * 4;
+    if (M <= kDecodeMaxM) part = std::max(part, decode_partial_bytes(N, K));
+    w.part = piece(part);
+    w.b8 = piece(r % 8 ? (size_t)n * N * round_up(r, 8) * 2 : 0);
+    w.dy8 = piece(N % 8 ? (size_t)M * round_up(N, 8) * 2 : 0);
+    w.total = o;
+    return w;
+}
+
+AdapterLists lists_at(char* ws, const AdaptersWs& w) {
+    AdapterLists l;
+    l.tok = reinterpret_cast<int32_t*>(ws + w.tok);
+    l.n512 = reinterpret_cast<uint32_t*>(ws + w.n512);
+    l.e512 = reinterpret_cast<uint32_t*>(ws + w.e512);
+    l.n128 = reinterpret_cast<uint32_t*>(ws + w.n128);
+    l.e128 = reinterpret_cast<uint32_t*>(ws + w.e128);
+    l.n_grad = reinterpret_cast<uint32_t*>(ws + w.n_grad);
+    l.e_grad = reinterpret_cast<uint4*>(ws + w.e_grad);
+    l.cap512 = w.cap512; l.cap128 = w.cap128; l.tiles64 = w.tiles64;
+    return l;
+}
+
+qlora_status launch_lists(const int32_t* idx, int64_t M, int32_t n, const AdaptersWs& w, const AdapterLists& l,
+                          bool grads, cudaStream_t s) {
+    uint32_t* err = device_error_word();
+    if (!err) return QLORA_ERR_CUDA;
+    (void)launch_dependent(build_lists, dim3((unsigned)(w.tiles512 + (grads ? n : 0))), dim3(512), 0, s, idx, M, n,
+                           w.tiles512, l, err);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+qlora_status launch_pad_rows(const void* in, int64_t rows, int64_t cols, void* out, cudaStream_t s) {
+    const int64_t cols_out = round_up(cols, 8), blocks = (rows * (cols_out / 8) + 255) / 256;
+    if (blocks > INT32_MAX) return QLORA_ERR_SHAPE;
+    (void)launch_dependent(pad_rows, dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const uint16_t*>(in), rows,
+                           cols, cols_out, static_cast<uint4*>(out));
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+template <bool V_MN>
+qlora_status launch_part(const CUtensorMap& tmS, const CUtensorMap& tmV, PartParams& p, int splits, cudaStream_t s) {
+    static bool configured = false;
+    auto kern = tc_part_gemm<V_MN>;
+    if (!configured) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        configured = true;
+    }
+    // two CTAs per SM up to 128 ranks: 4 + 5 stages of 16 + 8 KiB, or 3 + 3 of 16 + 16 KiB
+    p.s_stages = p.v_tile <= 8192 ? 4 : 3;
+    p.v_stages = p.v_tile <= 8192 ? 5 : 3;
+    const PartLayout lay = part_layout(p.s_stages, p.v_stages, p.v_tile);
+    if (lay.alloc > kMaxSmem) return QLORA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)((p.M + kPartTile - 1) / kPartTile), (unsigned)splits);
+    (void)launch_dependent(kern, grid, dim3(kPartThreads), lay.alloc, s, tmS, tmV, p);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+// partial = S V_a^T over the adapters: S [M, red] 16-bit with rows of ld elements; V = A_all
+// [n, r, red] (v_mn false) or B_all [n, red, ldv] with r of its ldv columns (v_mn true).
+// Returns the split count in *splits_out.
+qlora_status part_gemm(const void* S, int64_t M, int64_t red, int64_t ld, const void* V, bool v_mn, int64_t ldv,
+                       int32_t r, int32_t n, const AdapterLists& l, float* partial, bool f16, int* splits_out,
+                       cudaStream_t s) {
+    PartParams p{};
+    p.M = M;
+    p.Rn = (int32_t)round_up(r, 16);
+    p.ksteps_total = (int32_t)((red + 63) / 64);
+    const int splits = part_splits(M, red, r);
+    p.ksteps_per_split = (p.ksteps_total + splits - 1) / splits;
+    p.tmem_cols = p.Rn <= 32 ? 32u : p.Rn <= 64 ? 64u : p.Rn <= 128 ? 128u : 256u;
+    p.v_tile = v_mn ? (uint32_t)round_up(p.Rn, 64) * 128u : (uint32_t)p.Rn * 128u;
+    p.v_tile = (uint32_t)round_up(p.v_tile, 1024);            // swizzle atoms stay aligned
+    p.f16 = f16;
+    p.count = l.n128; p.entry = l.e128; p.cap = l.cap128; p.tok = l.tok;
+    p.partial = partial;
+    p.err = device_error_word();
+    if (!p.err) return QLORA_ERR_CUDA;
+    *splits_out = splits;
+    CUtensorMap tmS, tmV;
+    if (!make_tmap_2d(&tmS, true, S, red, M, ld * 2, 64, 128, true)) return QLORA_ERR_CUDA;
+    if (v_mn) {
+        if (!make_tmap_3d(&tmV, V, ldv, red, n, 64, 64)) return QLORA_ERR_CUDA;
+        return launch_part<true>(tmS, tmV, p, splits, s);
+    }
+    if (!make_tmap_3d(&tmV, V, red, r, n, 64, (uint32_t)p.Rn)) return QLORA_ERR_CUDA;
+    return launch_part<false>(tmS, tmV, p, splits, s);
+}
+
+qlora_status launch_finish(const float* partial, int splits, int64_t M, int32_t r, const AdapterLists& l,
+                           const float* scales, float* out, void* V2, bool f16, cudaStream_t s) {
+    const int32_t R = half_width(r);
+    const int64_t blocks = (M * R + 255) / 256;
+    if (blocks > INT32_MAX) return QLORA_ERR_SHAPE;
+    (void)launch_dependent(finish_part, dim3((unsigned)blocks), dim3(256), 0, s, partial, splits, M, (int)r,
+                           (int)round_up(r, 16), (int)R, (const int32_t*)l.tok, scales, out, static_cast<uint16_t*>(V2),
+                           f16);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M, int64_t N, int64_t K, int32_t r,
+                          int32_t n, const void* dU2, const void* U2, const AdapterLists& l, bool f16, float* dA,
+                          float* dB, cudaStream_t s) {
+    static bool configured = false;
+    if (!configured) {
+        if (cudaFuncSetAttribute(tc_adapter_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) !=
+            cudaSuccess)
+            return QLORA_ERR_CUDA;
+        configured = true;
+    }
+    GradParams p{};
+    const int64_t R = half_width(r);
+    p.M = M; p.K = K; p.N = N; p.r = r; p.R = (int32_t)R;
+    p.tiles_k = (int32_t)((K + 127) / 128);
+    const int64_t tiles = p.tiles_k + (N + 127) / 128;
+    if (tiles > INT32_MAX || n > 65535) return QLORA_ERR_SHAPE;
+    p.v_bytes = (uint32_t)(2 * R / 64) * 8192u;
+    p.tmem_cols = R <= 32 ? 64u : R <= 64 ? 128u : 256u;
+    // as many stages as fit in half of the shared memory (two CTAs per SM), else one CTA's worth
+    uint32_t stages = (kMaxSmem / 2 - 3072) / (kStage16K + p.v_bytes);
+    if (stages < 2) stages = (kMaxSmem - 3072) / (kStage16K + p.v_bytes);
+    p.stages = std::min(stages, 4u);
+    p.f16 = f16;
+    p.n_grad = l.n_grad; p.e_grad = l.e_grad; p.tiles64 = l.tiles64;
+    p.dA = dA; p.dB = dB;
+    p.err = device_error_word();
+    if (!p.err) return QLORA_ERR_CUDA;
+    CUtensorMap tmX, tmdY, tmdU2, tmU2;
+    if (!make_tmap_2d(&tmX, true, X, K, M, K * 2, 64, 64, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmdY, true, dY, N, M, ldy * 2, 64, 64, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmdU2, true, dU2, 2 * R, M, 4 * R, 64, 64, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmU2, true, U2, 2 * R, M, 4 * R, 64, 64, true)) return QLORA_ERR_CUDA;
+    const GradLayout lay = grad_layout(p.stages, p.v_bytes);
+    (void)launch_dependent(tc_adapter_grads, dim3((unsigned)tiles, (unsigned)n), dim3(kGradThreads), lay.alloc, s, tmX,
+                           tmdY, tmdU2, tmU2, p);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
+
+// Checks that the entry points below share; n_adapters planes of B_all are rows of one tensor map.
+qlora_status check_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int32_t n) {
+    QLORA_TRY(check_shape(N, K));
+    QLORA_TRY(check_lora(M, r, 1.0f));
+    if (n < 1 || n > 65535) return QLORA_ERR_INVALID_ARG;
+    if (M > INT32_MAX - 512 || (int64_t)n * N > INT32_MAX - 512) return QLORA_ERR_SHAPE;
+    return QLORA_OK;
+}
+
+// The fused GEMM of gemm_tc.cu over the tile lists: the forward (dx false) or dX.
+qlora_status adapters_gemm(const qlora_nf4_weight* w, const void* A0, int64_t ld0, int64_t M, const void* V2, const void* B1,
+                           int32_t b1_r, int32_t r, int32_t n, const AdapterLists& l, void* out, int32_t out_dtype,
+                           bool dx, cudaStream_t s) {
+    TcGemmArgs a{};
+    a.w = w; a.A0 = A0; a.a0_ld = ld0; a.A1 = V2; a.B1 = B1; a.b1_r = b1_r; a.Rpad = half_width(r); a.n_adapters = n;
+    a.p.M = M;
+    a.p.Nout = dx ? w->K : w->N;
+    a.p.ldo = a.p.Nout;
+    a.p.out = out;
+    a.p.out_f32 = out_dtype == QLORA_DTYPE_F32;
+    a.p.ad.count = l.n512; a.p.ad.entry = l.e512; a.p.ad.cap = l.cap512;
+    return launch_tc_gemm_nf4(a, dx, s);
+}
+
+}  // namespace
+}  // namespace qlora
+
+using namespace qlora;
+
+extern "C" {
+
+qlora_status qlora_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r, int32_t n_adapters,
+                                           size_t* bytes) {
+    QLORA_TRY(check_adapters(M, N, K, r, n_adapters));
+    if (!bytes) return QLORA_ERR_INVALID_ARG;
+    *bytes = adapters_ws(M, N, K, r, n_adapters).total;
+    return QLORA_OK;
+}
+
+qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X, int64_t M, const void* A_all,
+                                       const void* B_all, int32_t n_adapters, const int32_t* adapter_idx, int32_t r,
+                                       const float* scales, void* Y, int32_t y_dtype, float* U_save, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    QLORA_TRY(check_weight(w));
+    const int64_t N = w->N, K = w->K;
+    QLORA_TRY(check_adapters(M, N, K, r, n_adapters));
+    QLORA_TRY(check_dev(X));
+    QLORA_TRY(check_dev(A_all));
+    QLORA_TRY(check_dev(B_all));
+    if (!adapter_idx || !scales) return QLORA_ERR_INVALID_ARG;
+    if (!aligned_to(adapter_idx, 4) || !aligned_to(scales, 4)) return QLORA_ERR_ALIGN;
+    QLORA_TRY(check_dev(Y));
+    QLORA_TRY(check_out_dtype(y_dtype, w));
+    if (U_save && !aligned16(U_save)) return QLORA_ERR_ALIGN;
+    const AdaptersWs lw = adapters_ws(M, N, K, r, n_adapters);
+    if (!workspace || workspace_bytes < lw.total) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    float* partial = reinterpret_cast<float*>(ws + lw.part);
+    float* U = U_save ? U_save : reinterpret_cast<float*>(ws + lw.u);
+    const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
+    if (M <= kDecodeMaxM) {
+        DecodeArgs d{};
+        d.w = w; d.X = X; d.A = A_all; d.B = B_all; d.r = r; d.scale = 0.f; d.scales = scales; d.M = M; d.out = Y;
+        d.out_f32 = (y_dtype == QLORA_DTYPE_F32);
+        d.U = U; d.partial = partial; d.aidx = adapter_idx; d.n_adapters = n_adapters;
+        TimerScope t(QLORA_TIMER_DECODE, s);
+        return launch_tc_decode(d, s);
+    }
+    const AdapterLists l = lists_at(ws, lw);
+    void* U2 = ws + lw.u2;
+    const void* B8 = B_all;
+    {
+        TimerScope t(QLORA_TIMER_LORA, s);
+        QLORA_TRY(launch_lists(adapter_idx, M, n_adapters, lw, l, false, s));
+        if (r % 8) {
+            QLORA_TRY(launch_pad_rows(B_all, n_adapters * N, r, ws + lw.b8, s));
+            B8 = ws + lw.b8;
+        }
+        int splits = 0;
+        QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
+        QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, U_save, U2, f16, s));
+    }
+    TimerScope t(QLORA_TIMER_FWD_MAIN, s);
+    return adapters_gemm(w, X, K, M, U2, B8, (int32_t)round_up(r, 8), r, n_adapters, l, Y, y_dtype, false, s);
+}
+
+qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X, const void* dY, int64_t M,
+                                       const void* A_all, const void* B_all, int32_t n_adapters,
+                                       const int32_t* adapter_idx, int32_t r, const float* scales,
+                                       const float* U_saved, void* dX, int32_t dx_dtype, float* dA_all, float* dB_all,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+    QLORA_TRY(check_weight(w));
+    const int64_t N = w->N, K = w->K;
+    QLORA_TRY(check_adapters(M, N, K, r, n_adapters));
+    QLORA_TRY(check_dev(X));
+    QLORA_TRY(check_dev(dY));
+    QLORA_TRY(check_dev(A_all));
+    QLORA_TRY(check_dev(B_all));
+    if (!adapter_idx || !scales) return QLORA_ERR_INVALID_ARG;
+    if (!aligned_to(adapter_idx, 4) || !aligned_to(scales, 4)) return QLORA_ERR_ALIGN;
+    QLORA_TRY(check_dev(dA_all));
+    QLORA_TRY(check_dev(dB_all));
+    if (dX) {
+        QLORA_TRY(check_dev(dX));
+        QLORA_TRY(check_out_dtype(dx_dtype, w));
+    }
+    if (U_saved && !aligned16(U_saved)) return QLORA_ERR_ALIGN;
+    const AdaptersWs lw = adapters_ws(M, N, K, r, n_adapters);
+    if (!workspace || workspace_bytes < lw.total) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    float* partial = reinterpret_cast<float*>(ws + lw.part);
+    const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
+    const AdapterLists l = lists_at(ws, lw);
+    void* U2 = ws + lw.u2;
+    void* dU2 = ws + lw.du2;
+    const void* B8 = B_all;
+    const void* dY8 = dY;
+    const int64_t ldy = round_up(N, 8);
+    {
+        TimerScope t(QLORA_TIMER_LORA, s);
+        QLORA_TRY(launch_lists(adapter_idx, M, n_adapters, lw, l, true, s));
+        if (r % 8) {
+            QLORA_TRY(launch_pad_rows(B_all, n_adapters * N, r, ws + lw.b8, s));
+            B8 = ws + lw.b8;
+        }
+        if (N % 8) {
+            QLORA_TRY(launch_pad_rows(dY, M, N, ws + lw.dy8, s));
+            dY8 = ws + lw.dy8;
+        }
+        int splits = 0;
+        if (!U_saved) {
+            QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
+            QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, nullptr, U2, f16, s));
+        } else {
+            QLORA_TRY(launch_finish(U_saved, 0, M, r, l, scales, nullptr, U2, f16, s));
+        }
+        QLORA_TRY(part_gemm(dY8, M, N, ldy, B8, true, round_up(r, 8), r, n_adapters, l, partial, f16, &splits, s));
+        QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, nullptr, dU2, f16, s));
+    }
+    // the adapter gradients run beside dX on the low-priority side stream and fill the SMs that its
+    // last wave of tiles leaves idle
+    cudaStream_t g = dX ? side_stream() : s;
+    cudaEvent_t join = nullptr;
+    if (dX) {
+        if (!g) return QLORA_ERR_CUDA;
+        cudaEvent_t fork = nullptr;
+        if (cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) != cudaSuccess) return QLORA_ERR_CUDA;
+        bool ok = cudaEventCreateWithFlags(&join, cudaEventDisableTiming) == cudaSuccess;
+        ok = ok && cudaEventRecord(fork, s) == cudaSuccess && cudaStreamWaitEvent(g, fork, 0) == cudaSuccess;
+        cudaEventDestroy(fork);
+        if (!ok) {
+            if (join) cudaEventDestroy(join);
+            return QLORA_ERR_CUDA;
+        }
+    }
+    qlora_status st = QLORA_OK;
+    if (dX) {
+        TimerScope t(QLORA_TIMER_DX_MAIN, s);
+        st = adapters_gemm(w, dY8, ldy, M, dU2, A_all, r, r, n_adapters, l, dX, dx_dtype, true, s);
+    }
+    if (st == QLORA_OK) {
+        TimerScope t(QLORA_TIMER_LORA, g);
+        st = launch_grads(X, dY8, ldy, M, N, K, r, n_adapters, dU2, U2, l, f16, dA_all, dB_all, g);
+    }
+    if (dX) {   // the caller's stream resumes after the adapter gradients too
+        const bool ok = cudaEventRecord(join, g) == cudaSuccess && cudaStreamWaitEvent(s, join, 0) == cudaSuccess;
+        cudaEventDestroy(join);
+        if (!ok && st == QLORA_OK) st = QLORA_ERR_CUDA;
+    }
+    return st;
+}
+
+}  // extern "C"

@@ -75,7 +75,7 @@ namespace {
 
 std::atomic<uint64_t> g_launches{0};
 
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+}  // namespace
 
 qlora_status check_lora(int64_t M, int32_t r, float alpha) {
     if (M < 1 || M > (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
@@ -83,6 +83,8 @@ qlora_status check_lora(int64_t M, int32_t r, float alpha) {
     if (!std::isfinite(alpha)) return QLORA_ERR_INVALID_ARG;
     return QLORA_OK;
 }
+
+namespace {
 
 // LoRA rank padded to a multiple of 64 (each hi/lo half fills whole 64-wide reduction steps).
 inline int32_t rank_pad(int32_t r) { return (r + 63) / 64 * 64; }
@@ -133,6 +135,8 @@ qlora_status lora_U(const void* X, const void* A, int64_t M, int64_t K, int32_t 
     return launch_reduce_rows(partial, splits, M, r, R, 1.f, U, s_lora, U2, f16, s);
 }
 
+}  // namespace
+
 // The backward's adapter-gradient work (dA, dB and their reductions) runs on a second stream of
 // the lowest priority, forked from the caller's stream after dU is ready and joined back before
 // the call returns: it reads only dU, X, dY and U, none of which the dX GEMM writes, so it can
@@ -154,6 +158,8 @@ cudaStream_t side_stream() {
     }
     return streams[dev];
 }
+
+namespace {
 
 // dA = dU^T X (computed as dA^T [K, R] = X^T dU) and dB = s dY^T U = dY^T (s U) from the hi/lo
 // operands dU2 and U2, on stream g; both use the split-partial region in turn.
@@ -182,12 +188,12 @@ qlora_status lora_gradients_tc(const void* X, const void* dY, int64_t M, int64_t
     return QLORA_OK;
 }
 
+}  // namespace
+
 // Output dtypes a layer may write: fp32, or its 16-bit compute dtype.
 qlora_status check_out_dtype(int32_t dt, const qlora_nf4_weight* w) {
     return (dt == QLORA_DTYPE_F32 || dt == w->compute_dtype) ? QLORA_OK : QLORA_ERR_INVALID_ARG;
 }
-
-}  // namespace
 
 void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 

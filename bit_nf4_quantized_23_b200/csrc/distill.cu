@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 4) distill_bwd(DistillParams p) {
     constexpr int kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2, kEd = DT_OUT == QLORA_DTYPE_F32 ? 4 : 2;
     const char* row = static_cast<const char*>(p.logits) + m * p.ld * kEs;
     char* drow = static_cast<char*>(p.dlogits) + m * p.ldd * kEd;
-    // VEC: both rows are 16-byte aligned `head` elements in, for the same head in 0 .. 7
-    const int64_t head = VEC ? min(p.V, (int64_t)((8 - (m * p.ld & 7)) & 7)) : 0;
+    // VEC: both rows are 16-byte aligned `head` elements in, as the narrower type's address says
+    const uintptr_t at = reinterpret_cast<uintptr_t>(kEd <= kEs ? drow : row);
+    const int64_t head = VEC ? min(p.V, (int64_t)(((16u - (uint32_t)(at & 15u)) & 15u) / (kEd <= kEs ? kEd : kEs))) : 0;
     const int64_t chunks = VEC ? (p.V - head) / 8 : 0;
     const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
     const bool last = part == p.parts - 1;
@@ -450,8 +451,14 @@ cudaError_t run_fwd(const DistillParams& p, cudaStream_t s) {
 template <int DT_IN, int DT_OUT>
 cudaError_t run_bwd2(const DistillParams& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.M * p.parts));
-    // chunks of eight are 16-byte aligned in both rows when the row strides agree modulo eight
-    if (((p.ld ^ p.ldd) & 7) == 0) return launch_dependent(distill_bwd<DT_IN, DT_OUT, true>, grid, dim3(kThreads), 0, s, p);
+    // chunks of eight are 16-byte aligned in both rows when the rows' first elements lie alike modulo
+    // 16 bytes of the wider type
+    constexpr int64_t kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2, kEd = DT_OUT == QLORA_DTYPE_F32 ? 4 : 2;
+    constexpr int64_t kPer16 = 16 / (kEs > kEd ? kEs : kEd);
+    const int64_t z0 = (int64_t)(reinterpret_cast<uintptr_t>(p.logits) & 15u) / kEs;
+    const int64_t d0 = (int64_t)(reinterpret_cast<uintptr_t>(p.dlogits) & 15u) / kEd;
+    if ((z0 - d0) % kPer16 == 0 && (p.ld - p.ldd) % kPer16 == 0)
+        return launch_dependent(distill_bwd<DT_IN, DT_OUT, true>, grid, dim3(kThreads), 0, s, p);
     return launch_dependent(distill_bwd<DT_IN, DT_OUT, false>, grid, dim3(kThreads), 0, s, p);
 }
 
@@ -462,15 +469,21 @@ cudaError_t run_bwd(const DistillParams& p, int d_dtype, cudaStream_t s) {
     return run_bwd2<DT_IN, QLORA_DTYPE_BF16>(p, s);
 }
 
+// A device pointer of elements of `bytes` bytes: present and aligned to them.
+qlora_status check_elems(const void* p, int bytes) {
+    if (!p) return QLORA_ERR_INVALID_ARG;
+    return aligned_to(p, (uintptr_t)bytes) ? QLORA_OK : QLORA_ERR_ALIGN;
+}
+
 bool dtype_ok(int32_t dt) { return dt == QLORA_DTYPE_BF16 || dt == QLORA_DTYPE_F16 || dt == QLORA_DTYPE_F32; }
 
 // The checks that both directions share; fills the common parameters.
 qlora_status distill_args(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V, const int32_t* idx,
                           const void* t, int32_t t_dtype, int32_t k, float T, DistillParams& p) {
-    QLORA_TRY(check_dev(logits));
-    QLORA_TRY(check_dev(idx));
-    QLORA_TRY(check_dev(t));
     if (!dtype_ok(z_dtype) || !dtype_ok(t_dtype)) return QLORA_ERR_INVALID_ARG;
+    QLORA_TRY(check_elems(logits, elem_size(z_dtype)));
+    QLORA_TRY(check_elems(idx, 4));
+    QLORA_TRY(check_elems(t, elem_size(t_dtype)));
     if (k < 1 || k > kMaxTop) return QLORA_ERR_INVALID_ARG;
     // 1/T^2 and T^2 stay normal fp32 numbers within these limits
     if (!(T >= 1e-3f && T <= 1e3f)) return QLORA_ERR_INVALID_ARG;
@@ -495,8 +508,8 @@ qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t
                                     float temperature, float* loss, float* lse, void* stream) {
     DistillParams p{};
     QLORA_TRY(distill_args(logits, z_dtype, ld, M, V, teacher_idx, teacher_logits, t_dtype, k, temperature, p));
-    QLORA_TRY(check_dev(loss));
-    QLORA_TRY(check_dev(lse));
+    QLORA_TRY(check_elems(loss, 4));
+    QLORA_TRY(check_elems(lse, 4));
     p.loss = loss; p.lse = lse;
     p.err = device_error_word();
     if (!p.err) return QLORA_ERR_CUDA;
@@ -514,10 +527,10 @@ qlora_status qlora_distill_topk_bwd(const void* logits, int32_t z_dtype, int64_t
                                     int32_t d_dtype, int64_t ldd, void* stream) {
     DistillParams p{};
     QLORA_TRY(distill_args(logits, z_dtype, ld, M, V, teacher_idx, teacher_logits, t_dtype, k, temperature, p));
-    QLORA_TRY(check_dev(lse));
-    QLORA_TRY(check_dev(dloss));
-    QLORA_TRY(check_dev(dlogits));
     if (!dtype_ok(d_dtype)) return QLORA_ERR_INVALID_ARG;
+    QLORA_TRY(check_elems(lse, 4));
+    QLORA_TRY(check_elems(dloss, 4));
+    QLORA_TRY(check_elems(dlogits, elem_size(d_dtype)));
     if (ldd < V || ldd > (int64_t(1) << 40) / M) return QLORA_ERR_SHAPE;
     // in place (the same rows of the same type) or apart: anything between would read written values
     const uintptr_t z0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(dlogits);

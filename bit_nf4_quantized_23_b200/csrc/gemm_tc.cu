@@ -216,7 +216,25 @@ __device__ __forceinline__ void store_row32(const TcGemmParams& p, int64_t m, in
     }
 }
 
-template <int NUM_ACC, bool DX>
+// The row mask of a tile's adapter, inverted (a set bit keeps its accumulator row as it is): `words`
+// words from word `first` of entry e.
+template <int WORDS>
+__device__ __forceinline__ void load_lanes_off(const uint32_t* entry, uint32_t (&off)[WORDS]) {
+#pragma unroll
+    for (int w = 0; w < WORDS / 4; ++w) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(entry) + w);
+        off[4 * w] = ~v.x;
+        off[4 * w + 1] = ~v.y;
+        off[4 * w + 2] = ~v.z;
+        off[4 * w + 3] = ~v.w;
+    }
+}
+
+// MULTI: every token has its own adapter (or none).  The tile's list names the adapters that its
+// tokens use; each adds its LoRA steps with that adapter's B (forward) or A (dX) as operand B, and
+// its MMAs update only the accumulator rows of its own tokens (tcgen05.mma's output-lane mask), so
+// no operand is masked or copied and a token never meets another request's adapter.
+template <int NUM_ACC, bool DX, bool MULTI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmCodes,
             const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1, TcGemmParams p) {
@@ -239,7 +257,8 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
     raster_tile(blockIdx.x, (p.M + L::kBM - 1) / L::kBM, (p.Nout + kBN - 1) / kBN, mt, nt);
     const int64_t n0 = nt * kBN;                          // output column tile
     const int64_t m0 = mt * L::kBM;                       // output row tile
-    const int ks0 = p.ksteps0, ktotal = p.ksteps0 + p.ksteps1;
+    const uint32_t* const ad_list = MULTI ? p.ad.entry + (m0 / kAdTile) * p.ad.cap * kAdEntry : nullptr;
+    const int ks0 = p.ksteps0, ktotal = p.ksteps0 + (MULTI ? (int)p.ad.count[m0 / kAdTile] : 1) * p.ksteps1;
     float* e4tab = reinterpret_cast<float*>(gbase + L::kE4);
     if (threadIdx.x < 256) e4tab[threadIdx.x] = e4m3_to_f32(threadIdx.x);
 
@@ -273,7 +292,14 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         int issued = 0;
         int s = 0;
         uint32_t ph = 0;
+        int je = -1, adapter = 0;                             // MULTI: LoRA step of the adapter at hand
+        const uint32_t* ad_entry = ad_list;
         for (int it = 0; it < ktotal; ++it) {
+            if (MULTI && it >= ks0 && (it == ks0 || ++je == p.ksteps1)) {
+                je = 0;
+                adapter = (int)__ldg(ad_entry + 16);
+                ad_entry += kAdEntry;
+            }
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * s, ph ^ 1u, abort, p.err))) break;
             issued = it + 1;
             if (ptx::elect_one_sync()) {
@@ -286,16 +312,18 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                     if (!DX) ptx::tma_load_2d(sCodes + s * kCodesStageBytes, &tmCodes, it * 32, (int32_t)n0, fa);
                     else ptx::tma_load_2d(sCodes + s * kCodesStageBytes, &tmCodes, (int32_t)(n0 / 2), it * 64, fa);
                 } else {
-                    const int j = it - ks0;
+                    const int j = MULTI ? je : it - ks0;
                     const int jb = p.b1_wrap ? j % p.b1_wrap : j;   // hi and lo steps share the B1 tile
                     ptx::mbar_arrive_expect_tx(fa, L::kAStageBytes + kBStageBytes);
                     ptx::tma_load_2d(a_dst, &tmA1, j * 64, (int32_t)m0, fa);
                     if (!DX) {
-                        ptx::tma_load_2d(b_dst, &tmB1, jb * 64, (int32_t)n0, fa);
+                        ptx::tma_load_2d(b_dst, &tmB1, jb * 64, (int32_t)n0 + (MULTI ? adapter * p.ad.rows : 0), fa);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            ptx::tma_load_2d(b_dst + c * 8192, &tmB1, (int32_t)(n0 + c * 64), jb * 64, fa);
+                        for (int c = 0; c < 4; ++c) {
+                            if (MULTI) ptx::tma_load_3d(b_dst + c * 8192, &tmB1, (int32_t)(n0 + c * 64), jb * 64, adapter, fa);
+                            else ptx::tma_load_2d(b_dst + c * 8192, &tmB1, (int32_t)(n0 + c * 64), jb * 64, fa);
+                        }
                     }
                 }
             }
@@ -318,7 +346,19 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
         bool ok = true;
         int s = 0;
         uint32_t ph = 0;
+        // MULTI: lanes that the adapter at hand leaves alone, and the next adapter's, loaded ahead
+        int je = -1;
+        uint32_t off[NUM_ACC][4] = {}, off_next[4 * NUM_ACC] = {};
+        const uint32_t* ad_entry = MULTI ? ad_list + (m0 % kAdTile) / 32 : nullptr;
+        if (MULTI && ktotal > ks0) load_lanes_off<4 * NUM_ACC>(ad_entry, off_next);
         for (int it = 0; it < ktotal && ok; ++it) {
+            if (MULTI && it >= ks0 && (it == ks0 || ++je == p.ksteps1)) {
+                je = 0;
+#pragma unroll
+                for (int i = 0; i < 4 * NUM_ACC; ++i) off[i / 4][i % 4] = off_next[i];
+                ad_entry += kAdEntry;
+                if (it + p.ksteps1 < ktotal) load_lanes_off<4 * NUM_ACC>(ad_entry, off_next);
+            }
             bool w = ptx::mbar_wait(bar_full_a + 8 * s, ph, abort, p.err);
             if (w && it < ks0) w = ptx::mbar_wait(bar_full_b + 8 * s, ph, abort, p.err);
             ok = __all_sync(0xffffffffu, w);
@@ -329,13 +369,24 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 const bool kn = !DX && it < ks0;
                 const uint64_t bd = (kn ? bdesc0_kn : bdesc0) + ((uint32_t)s * (kBStageBytes >> 4));
                 const uint32_t kstep = DX ? (2048 >> 4) : kn ? ((2 * kBN * 16) >> 4) : (32 >> 4);
+                if (MULTI && it >= ks0) {
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t bdesc = bd + (p.ad.packed ? kk & 1 : kk) * kstep;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t bdesc = bd + kk * kstep;
+                        for (int h = 0; h < NUM_ACC; ++h)
+                            if ((off[h][0] & off[h][1] & off[h][2] & off[h][3]) != 0xFFFFFFFFu)
+                                ptx::mma_bf16_ss_lanes(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4), bdesc,
+                                                       idesc, 1u, off[h]);
+                    }
+                } else {
 #pragma unroll
-                    for (int h = 0; h < NUM_ACC; ++h)
-                        ptx::mma_bf16_ss(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4), bdesc, idesc,
-                                         (it | kk) != 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t bdesc = bd + kk * kstep;
+#pragma unroll
+                        for (int h = 0; h < NUM_ACC; ++h)
+                            ptx::mma_bf16_ss(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4), bdesc, idesc,
+                                             (it | kk) != 0 ? 1u : 0u);
+                    }
                 }
                 ptx::mma_commit(bar_empty + 8 * s);
             }
@@ -503,7 +554,7 @@ constexpr uint32_t kPairOffAbort = kPairOffSlot + 4;
 constexpr uint32_t kPairAlloc = kPairOffAbort + 4 + 1024;
 static_assert(kPairAlloc <= 232448, "shared memory of one CTA");
 
-template <bool DX>
+template <bool DX, bool MULTI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmCodes,
                  const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1, TcGemmParams p) {
@@ -531,7 +582,8 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
     const int64_t m0 = mt * 512 + 256 * (int64_t)rank;       // this CTA's first token
     const int64_t n0 = nt * bn;                               // the pair's output column tile
     const int64_t nr0 = n0 + hb * (int64_t)rank;              // this CTA's output columns (forward: W rows)
-    const int ks0 = p.ksteps0, ktotal = p.ksteps0 + p.ksteps1;
+    const uint32_t* const ad_list = MULTI ? p.ad.entry + mt * p.ad.cap * kAdEntry : nullptr;   // a pair's tile is kAdTile
+    const int ks0 = p.ksteps0, ktotal = p.ksteps0 + (MULTI ? (int)p.ad.count[mt] : 1) * p.ksteps1;
     float* e4tab = reinterpret_cast<float*>(gbase + kPairOffE4);
     if (threadIdx.x < 256) e4tab[threadIdx.x] = e4m3_to_f32(threadIdx.x);
 
@@ -568,7 +620,14 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
         int issued = 0;
         int s = 0;
         uint32_t ph = 0;
+        int je = -1, adapter = 0;                             // MULTI: LoRA step of the adapter at hand
+        const uint32_t* ad_entry = ad_list;
         for (int it = 0; it < ktotal; ++it) {
+            if (MULTI && it >= ks0 && (it == ks0 || ++je == p.ksteps1)) {
+                je = 0;
+                adapter = (int)__ldg(ad_entry + 16);
+                ad_entry += kAdEntry;
+            }
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * s, ph ^ 1u, abort, p.err))) break;
             issued = it + 1;
             if (ptx::elect_one_sync()) {
@@ -583,19 +642,25 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                         ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, (int32_t)(nr0 / 2), it * 64,
                                          bar_codes + 8 * s);
                 } else {
-                    const int j = it - ks0;
+                    const int j = MULTI ? je : it - ks0;
                     const int jb = p.b1_wrap ? j % p.b1_wrap : j;   // hi and lo steps share the B1 tile
                     if (leader)
                         ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s,
                                                    2 * (kPairAStage + (DX ? kPairBStage : 128u * (uint32_t)hb)));
                     ptx::tma_load_2d_pair(a_dst, &tmA1, j * 64, (int32_t)m0, lead_full_a + 8 * s);
                     if (!DX) {
-                        ptx::tma_load_2d_pair(sB + s * kPairBStage, &tmB1, jb * 64, (int32_t)nr0, lead_full_a + 8 * s);
+                        ptx::tma_load_2d_pair(sB + s * kPairBStage, &tmB1, jb * 64,
+                                              (int32_t)nr0 + (MULTI ? adapter * p.ad.rows : 0), lead_full_a + 8 * s);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            ptx::tma_load_2d_pair(sB + s * kPairBStage + c * 8192, &tmB1, (int32_t)(nr0 + c * 64), jb * 64,
-                                                  lead_full_a + 8 * s);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t dst = sB + s * kPairBStage + c * 8192;
+                            if (MULTI)
+                                ptx::tma_load_3d_pair(dst, &tmB1, (int32_t)(nr0 + c * 64), jb * 64, adapter,
+                                                      lead_full_a + 8 * s);
+                            else
+                                ptx::tma_load_2d_pair(dst, &tmB1, (int32_t)(nr0 + c * 64), jb * 64, lead_full_a + 8 * s);
+                        }
                     }
                 }
             }
@@ -623,7 +688,20 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
             bool ok = true;
             int s = 0;
             uint32_t ph = 0;
+            // MULTI: lanes that the adapter at hand leaves alone (accumulator h: 128 tokens of each CTA
+            // of the pair), and the next adapter's 512, loaded ahead
+            int je = -1;
+            uint32_t off[2][8] = {}, off_next[16] = {};
+            const uint32_t* ad_entry = ad_list;
+            if (MULTI && ktotal > ks0) load_lanes_off<16>(ad_entry, off_next);
             for (int it = 0; it < ktotal && ok; ++it) {
+                if (MULTI && it >= ks0 && (it == ks0 || ++je == p.ksteps1)) {
+                    je = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) off[(i >> 2) & 1][(i & 3) + 4 * (i >> 3)] = off_next[i];
+                    ad_entry += kAdEntry;
+                    if (it + p.ksteps1 < ktotal) load_lanes_off<16>(ad_entry, off_next);
+                }
                 bool w = ptx::mbar_wait(bar_full_a + 8 * s, ph, abort, p.err);
                 if (w && it < ks0) w = ptx::mbar_wait(bar_full_b + 8 * s, ph, abort, p.err);
                 ok = __all_sync(0xffffffffu, w);
@@ -634,12 +712,25 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                     const bool kn = !DX && it < ks0;
                     const uint64_t bd = (kn ? bdesc0_kn : bdesc0) + ((uint32_t)s * (kPairBStage >> 4));
                     const uint32_t kstep = DX ? (2048 >> 4) : kn ? ((2 * 128 * 16) >> 4) : (32 >> 4);
+                    if (MULTI && it >= ks0) {
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t bdesc = bd + (p.ad.packed ? kk & 1 : kk) * kstep;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t (&o)[8] = off[h];
+                                if ((o[0] & o[1] & o[2] & o[3] & o[4] & o[5] & o[6] & o[7]) != 0xFFFFFFFFu)
+                                    ptx::mma_bf16_ss_pair_lanes(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4),
+                                                                bdesc, idesc, 1u, o);
+                            }
+                        }
+                    } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            ptx::mma_bf16_ss_pair(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4),
-                                                  bd + kk * kstep, idesc, (it | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                ptx::mma_bf16_ss_pair(tmem + h * 256, ad + h * (16384 >> 4) + kk * (32 >> 4),
+                                                      bd + kk * kstep, idesc, (it | kk) != 0 ? 1u : 0u);
+                        }
                     }
                     ptx::mma_commit_pair(bar_empty + 8 * s);          // this CTA's stage
                     ptx::mma_commit_pair(peer_empty + 8 * s);         // the peer's stage
@@ -1126,7 +1217,7 @@ constexpr int kFixSlotBatch = 8;
 __global__ void __launch_bounds__(128)
 decode_fixup(const float* __restrict__ partial, int64_t units, int64_t G, int S, int64_t M, int64_t N,
              const float* __restrict__ U, const uint16_t* __restrict__ B, int r, float scale, void* out, int out_f32,
-             const int32_t* __restrict__ aidx, int n_adapters, bool f16) {
+             const int32_t* __restrict__ aidx, int n_adapters, const float* __restrict__ scales, bool f16) {
     extern __shared__ float us[];                             // us[j * 4 + q] = U[m0 + q, j]
     __shared__ int32_t tok_adapter[kFixTokens];
     const int m0 = (int)blockIdx.y * kFixTokens;
@@ -1211,7 +1302,8 @@ decode_fixup(const float* __restrict__ partial, int64_t units, int64_t G, int S,
     for (int q = 0; q < kFixTokens; ++q) {
         if (q < nm) {
             const int64_t m = m0 + q;
-            const float y = __fmaf_rn(scale, lora[q], acc[q]);
+            const int a = tok_adapter[q];
+            const float y = __fmaf_rn(scales && a >= 0 ? __ldg(scales + a) : scale, lora[q], acc[q]);
             if (out_f32) static_cast<float*>(out)[m * N + n] = y;
             else static_cast<uint16_t*>(out)[m * N + n] = (uint16_t)to16_rn(y, f16);
         }
@@ -1252,11 +1344,24 @@ bool make_tmap_2d(CUtensorMap* map, bool bf16, const void* base, uint64_t inner,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NUM_ACC, bool DX>
+bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
+                  uint32_t box1) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {d0, d1, d2};
+    const cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+    const cuuint32_t box[3] = {box0, box1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NUM_ACC, bool DX, bool MULTI>
 static qlora_status launch_one(const TcGemmArgs& a, cudaStream_t stream) {
     using L = Layout<NUM_ACC>;
     static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
-    auto kern = tc_gemm_nf4<NUM_ACC, DX>;
+    auto kern = tc_gemm_nf4<NUM_ACC, DX, MULTI>;
     if (!configured) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kAlloc) != cudaSuccess)
             return QLORA_ERR_CUDA;
@@ -1272,10 +1377,10 @@ static qlora_status launch_one(const TcGemmArgs& a, cudaStream_t stream) {
 }
 
 // The forward on CTA pairs: clusters of 2, one pair per 512 x 256 output tile.
-template <bool DX>
+template <bool DX, bool MULTI>
 static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream) {
     static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
-    auto kern = tc_gemm_nf4_pair<DX>;
+    auto kern = tc_gemm_nf4_pair<DX, MULTI>;
     if (!configured) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairAlloc) != cudaSuccess)
             return QLORA_ERR_CUDA;
@@ -1336,9 +1441,9 @@ static int pair_tile_width(int64_t M, int64_t N) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaFuncSetAttribute(tc_gemm_nf4_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(tc_gemm_nf4_pair<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kPairAlloc) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, tc_gemm_nf4_pair<false>, &cfg) != cudaSuccess || n < 1) {
+            cudaOccupancyMaxActiveClusters(&n, tc_gemm_nf4_pair<false, false>, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
             n = sms / 2;
         }
@@ -1423,7 +1528,7 @@ qlora_status launch_tc_decode(const DecodeArgs& a, cudaStream_t stream) {
                            (size_t)a.r * kFixTokens * sizeof(float), stream,
                            (const float*)a.partial, p.units, p.grid, (int)p.ksteps, a.M, N, (const float*)a.U,
                            static_cast<const uint16_t*>(a.B), a.r, a.scale, a.out, (int)a.out_f32, a.aidx,
-                           (int)a.n_adapters, p.f16 != 0);
+                           (int)a.n_adapters, a.scales, p.f16 != 0);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
@@ -1437,10 +1542,10 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     const uint32_t wrows = pair ? (uint32_t)a.p.bn / 2 : 256;   // forward: W rows one CTA loads codes (and LoRA B rows) for
     // segment 0: A (X or dY) and the packed codes
     if (!dx) {
-        if (!make_tmap_2d(&a.tmA0, true, a.A0, K, a.p.M, K * 2, 64, bm, true)) return QLORA_ERR_CUDA;
+        if (!make_tmap_2d(&a.tmA0, true, a.A0, K, a.p.M, (a.a0_ld ? a.a0_ld : K) * 2, 64, bm, true)) return QLORA_ERR_CUDA;
         if (!make_tmap_2d(&a.tmCodes, false, w->codes, K / 2, N, K / 2, 32, wrows, false)) return QLORA_ERR_CUDA;
     } else {
-        if (!make_tmap_2d(&a.tmA0, true, a.A0, N, a.p.M, N * 2, 64, bm, true)) return QLORA_ERR_CUDA;
+        if (!make_tmap_2d(&a.tmA0, true, a.A0, N, a.p.M, (a.a0_ld ? a.a0_ld : N) * 2, 64, bm, true)) return QLORA_ERR_CUDA;
         if (pair) {   // this CTA's 64 bytes (two blocks) of each of the step's 64 W rows, unswizzled
             if (!make_tmap_2d(&a.tmCodes, false, w->codes, K / 2, N, K / 2, 64, 64, false)) return QLORA_ERR_CUDA;
         } else {
@@ -1450,7 +1555,18 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     // segment 1: LoRA operands, [M, 2R] and [N, 2R] (forward) or [2R, K] (dX)
     const int64_t R2 = 2 * (int64_t)a.Rpad;
     if (!make_tmap_2d(&a.tmA1, true, a.A1, R2, a.p.M, R2 * 2, 64, bm, true)) return QLORA_ERR_CUDA;
-    if (a.b1_r > 0) {   // B [N, r] or A [r, K] directly
+    if (a.n_adapters > 0) {   // B_all [n, N, r] as n N rows (rows past an adapter's N give columns that are not
+                              // stored), A_all [n, r, K] as planes (ranks past r read as zero)
+        const uint64_t r = (uint64_t)a.b1_r, n = (uint64_t)a.n_adapters;
+        if (!dx) {
+            if (!make_tmap_2d(&a.tmB1, true, a.B1, r, n * N, r * 2, 64, wrows, true)) return QLORA_ERR_CUDA;
+        } else {
+            if (!make_tmap_3d(&a.tmB1, a.B1, K, r, n, 64, 64)) return QLORA_ERR_CUDA;
+        }
+        a.p.ad.rows = (int32_t)N;
+        a.p.ad.packed = a.Rpad == 32;
+        a.p.b1_wrap = a.p.ad.packed ? 1 : (int32_t)(R2 / 128);
+    } else if (a.b1_r > 0) {   // B [N, r] or A [r, K] directly
         const uint64_t r = (uint64_t)a.b1_r;
         if (!dx) {
             if (!make_tmap_2d(&a.tmB1, true, a.B1, r, N, r * 2, 64, wrows, true)) return QLORA_ERR_CUDA;
@@ -1475,9 +1591,14 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     a.p.tb = host_tables(w->codebook);
     a.p.err = device_error_word();
     if (!a.p.err) return QLORA_ERR_CUDA;
-    if (pair) return dx ? launch_pair<true>(a, stream) : launch_pair<false>(a, stream);
-    if (bm == 256) return dx ? launch_one<2, true>(a, stream) : launch_one<2, false>(a, stream);
-    return dx ? launch_one<1, true>(a, stream) : launch_one<1, false>(a, stream);
+    if (a.n_adapters > 0) {
+        if (pair) return dx ? launch_pair<true, true>(a, stream) : launch_pair<false, true>(a, stream);
+        if (bm == 256) return dx ? launch_one<2, true, true>(a, stream) : launch_one<2, false, true>(a, stream);
+        return dx ? launch_one<1, true, true>(a, stream) : launch_one<1, false, true>(a, stream);
+    }
+    if (pair) return dx ? launch_pair<true, false>(a, stream) : launch_pair<false, false>(a, stream);
+    if (bm == 256) return dx ? launch_one<2, true, false>(a, stream) : launch_one<2, false, false>(a, stream);
+    return dx ? launch_one<1, true, false>(a, stream) : launch_one<1, false, false>(a, stream);
 }
 
 }  // namespace qlora

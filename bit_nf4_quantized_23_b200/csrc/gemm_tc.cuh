@@ -7,6 +7,19 @@
 
 namespace qlora {
 
+// The adapters that the tokens of a tile use, one list per tile of kAdTile tokens (adapters.cu):
+// an entry is 16 words of row mask (bit i of word w: token 32 w + i of the tile uses the adapter),
+// the adapter, and 3 unused words.
+constexpr int kAdTile = 512;
+constexpr int kAdEntry = 20;
+struct TileAdapters {
+    const uint32_t* count;  // [tiles]
+    const uint32_t* entry;  // [tiles][cap][kAdEntry]
+    int32_t cap;
+    int32_t rows;           // forward: rows of one adapter in B_all (N)
+    int32_t packed;         // hi and lo halves of 32 ranks each share one 64-wide step
+};
+
 struct TcGemmParams {
     int64_t M;              // output rows (tokens)
     int64_t Nout;           // output columns (N for the forward, K for dX)
@@ -26,17 +39,20 @@ struct TcGemmParams {
                             // supplies bn / 2 of them); 256 everywhere else
     uint32_t* err;
     NF4Tables tb;
+    TileAdapters ad;        // MULTI kernels: the adapters of each token tile (ksteps1, b1_wrap per adapter)
 };
 
 struct TcGemmArgs {
     const qlora_nf4_weight* w;
     const void* A0;         // X [M,K] (forward) or dY [M,N] (dX), bf16
+    int64_t a0_ld;          // elements between rows of A0 (0: its row length)
     const void* A1;         // U2 or dU2 [M, 2*Rpad], bf16
     const void* B1;         // B2 [N, 2*Rpad] (forward) or A2 [2*Rpad, K] (dX), bf16; or, with b1_r > 0,
                             // B [N, b1_r] / A [b1_r, K] themselves (the hi and lo steps read the same tile,
                             // ranks past b1_r read as zero; B needs b1_r % 8 == 0)
     int32_t b1_r;
-    int32_t Rpad;           // LoRA rank padded to a multiple of 64
+    int32_t Rpad;           // LoRA rank padded to a multiple of 64 (32 too with n_adapters > 0)
+    int32_t n_adapters;     // > 0: one adapter per token; B1 is B_all [n, N, b1_r] or A_all [n, b1_r, K] and p.ad is set
     TcGemmParams p;
     CUtensorMap tmA0, tmCodes, tmA1, tmB1;
 };
@@ -83,6 +99,7 @@ struct DecodeArgs {
     float* U;               // [M, r] fp32, written (X A^T)
     float* partial;         // decode_partial_bytes(N, K)
     const int32_t* aidx;    // multi-adapter: device [M] adapter of each token (-1: none); NULL: one adapter
+    const float* scales;    // multi-adapter: device [n_adapters] scale of each adapter, or NULL: `scale` for all
     int32_t n_adapters;     // multi-adapter: A is [n_adapters, r, K], B is [n_adapters, N, r]
 };
 
@@ -124,6 +141,9 @@ qlora_status launch_lora_gemm(const LoraGemmArgs& a, cudaStream_t stream);
 int lora_splits(int64_t rows, int ksteps_total, int R, bool mn_major);
 size_t lora_partial_bytes(int64_t rows, int64_t red, int R, bool mn_major);
 
+// Rank-3 map of a 16-bit [d2, d1, d0] array with contiguous rows, 128-byte swizzle, boxes one deep.
+bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
+                  uint32_t box1);
 bool make_tmap_2d(CUtensorMap* map, bool bf16, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
 

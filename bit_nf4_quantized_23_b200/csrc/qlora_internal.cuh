@@ -43,11 +43,20 @@ void note_launches(int n);
 // Host side: argument checks of the entry points (api.cu).  Each returns QLORA_OK or the status
 // the entry point reports: blocksizes (UNSUPPORTED), shape (SHAPE), a weight descriptor (pointers,
 // alignment, codebook, compute dtype), a device pointer (non-null, 16-byte aligned).
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 qlora_status check_blocks(int32_t bs, int32_t bs2);
 qlora_status check_shape(int64_t N, int64_t K);
 qlora_status check_weight(const qlora_nf4_weight* w);
 qlora_status check_dev(const void* p);
+qlora_status check_lora(int64_t M, int32_t r, float alpha);                // tokens, rank, finite alpha
+qlora_status check_out_dtype(int32_t dt, const qlora_nf4_weight* w);      // fp32 or the compute dtype
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Host side: the low-priority side stream of the current device, on which the backward's adapter
+// gradients run beside dX (api.cu; nullptr on failure).
+cudaStream_t side_stream();
 
 // Device error flag word (one per device that loaded the library).  Kernels in
 // quantize.cu set it directly; other kernels get its address as an argument.

@@ -279,7 +279,6 @@ dq_blocks(const float* __restrict__ c1, int64_t nb1, const double* __restrict__ 
     }
 }
 
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 

@@ -274,6 +274,57 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const void* X, const vo
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The layer with the adapters of many requests at once ([CH9] section "3. 一个底座，
+ * 多个适配器"): any number of tokens, each with its own adapter over the shared
+ * quantized base, forward and backward; a decode batch, prompts, both mixed, or the
+ * sequences of several fine-tuning jobs.  With a = adapter_idx[m], s_a = scales[a]:
+ *     U[m]  = X[m] A_a^T                  (fp32)
+ *     Y[m]  = X[m] W_hat^T + s_a U[m] B_a^T       (X[m] W_hat^T where a = -1)
+ *   M           tokens, 1 .. 2^31 - 513.  Requests whose tokens are contiguous are
+ *               fastest: each tile of tokens does the adapter work of every adapter in it.
+ *   A_all       device [n_adapters, r, K], B_all device [n_adapters, N, r], in the
+ *               compute dtype.  An adapter of a smaller rank is padded with
+ *               zeros to r (its gradients there are zeros).
+ *   adapter_idx device int32 [M]; negative: no adapter.  An index >= n_adapters is
+ *               treated as -1 and raises the device BOUNDS flag.
+ *   scales      device fp32 [n_adapters]: alpha / r of each adapter.
+ *   U_save      optional device fp32 [M, r] for the backward (zeros without adapter).
+ *   workspace   at least qlora_adapters_workspace_size bytes; its contents need not
+ *               start at any value, and calls that overlap on the GPU need their own.
+ * Neither other tokens nor other adapters change a token's results, Inf and NaN included.
+ * Other arguments as qlora_linear_fwd (adapter_idx and scales need 4-byte alignment).
+ * Errors: QLORA_ERR_INVALID_ARG for n_adapters outside 1 .. 65535, QLORA_ERR_SHAPE
+ * when n_adapters * N is above 2^31 - 513, and those of qlora_linear_fwd.
+ */
+qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X, int64_t M,
+                                       const void* A_all, const void* B_all, int32_t n_adapters,
+                                       const int32_t* adapter_idx, int32_t r, const float* scales,
+                                       void* Y, int32_t y_dtype, float* U_save,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward, through the frozen weight into every adapter:
+ *     dU[m] = s_a dY[m] B_a
+ *     dX[m] = dY[m] W_hat + dU[m] A_a             (dx_dtype; skipped when dX is NULL)
+ *     dA_a  = sum over the tokens m of adapter a of dU[m]^T X[m]
+ *     dB_a  = sum over the tokens m of adapter a of s_a dY[m]^T U[m]
+ *   U_saved  device fp32 [M, r] from the forward, or NULL to recompute it.
+ *   dA_all   device fp32 [n_adapters, r, K] and dB_all device fp32 [n_adapters, N, r],
+ *            overwritten; zeros for an adapter without tokens.  Deterministic.
+ * Other arguments and errors as qlora_linear_fwd_adapters.
+ */
+qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X, const void* dY, int64_t M,
+                                       const void* A_all, const void* B_all, int32_t n_adapters,
+                                       const int32_t* adapter_idx, int32_t r, const float* scales,
+                                       const float* U_saved, void* dX, int32_t dx_dtype,
+                                       float* dA_all, float* dB_all,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two calls above for the given shape.  Host only. */
+qlora_status qlora_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r, int32_t n_adapters,
+                                           size_t* bytes);
+
+/*
  * Merge trained adapters into the frozen weight for inference ([Q103]
  * follow-up 1; [QP] section 5: merging and requantizing can add error): with
  * s = alpha / r,
@@ -340,7 +391,8 @@ qlora_status qlora_dequantize_int8_absmax(const int8_t* codes, const float* alph
  *   teacher_logits  device [M, k] of t_dtype (any qlora_dtype).
  *   temperature     1e-3 .. 1e3.
  *   loss, lse       device fp32 [M], written; the backward reads lse.
- * Statistics and sums are fp32.  Deterministic.
+ * Pointers need the alignment of their elements only, so that a chunk of rows of any
+ * length can be passed.  Statistics and sums are fp32.  Deterministic.
  * Errors: QLORA_ERR_INVALID_ARG (null pointer, dtype, k, temperature),
  * QLORA_ERR_SHAPE (M < 1, V < 1 or above 2^31 - 1, ld < V, M * ld above 2^40),
  * QLORA_ERR_ALIGN.
@@ -359,8 +411,8 @@ qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t
  *             columns V .. ldd-1 are left as they are.  It may be the logits' own
  *             memory (same pointer, stride and element size); any other overlap is
  *             QLORA_ERR_INVALID_ARG.
- * Row strides that agree modulo 8 elements (equal ones do) take 16-byte accesses;
- * others are read and written element by element.
+ * Logits and gradient whose rows lie alike within 16 bytes (both contiguous, or both
+ * with the same padding) take 16-byte accesses, others element by element.
  * Other arguments and errors as qlora_distill_topk_fwd.
  */
 qlora_status qlora_distill_topk_bwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,

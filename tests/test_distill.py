@@ -42,9 +42,9 @@ def test_refusals_on_the_host():
 
     for f in (fwd, bwd):
         assert f(z=None) == E["QLORA_ERR_INVALID_ARG"]
-        assert f(z=FAKE + 2) == E["QLORA_ERR_ALIGN"]
+        assert f(z=FAKE + 1) == f(z=FAKE + 2, zt=1) == f(lse=FAKE + 2) == E["QLORA_ERR_ALIGN"]
         assert f(idx=None) == E["QLORA_ERR_INVALID_ARG"]
-        assert f(t=FAKE + 4) == E["QLORA_ERR_ALIGN"]
+        assert f(t=FAKE + 2) == E["QLORA_ERR_ALIGN"]
         assert f(lse=None) == E["QLORA_ERR_INVALID_ARG"]
         assert f(zt=3) == f(tt=-1) == E["QLORA_ERR_INVALID_ARG"]
         assert f(k=0) == f(k=1025) == E["QLORA_ERR_INVALID_ARG"]
@@ -167,6 +167,22 @@ def test_row_strides_and_columns_behind_the_row(pad, dpad, dt, out):
     buf = torch.full((M, V + dpad), 7.0, dtype=DT[out], device="cuda")
     check_case(z, idx, t, 1.0, dloss, DT[out], dlogits=buf[:, :V])
     assert torch.all(buf[:, V:] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("z0,d0", [(0, 0), (1, 1), (3, 0), (2, 6), (5, 1)])
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", "fp32"), ("bf16", "fp32")])
+def test_rows_that_start_anywhere(z0, d0, dt, out):
+    """A chunk of rows of a larger tensor with an odd row length starts at any element."""
+    M, V, k = 4, 1003, 7
+    z, idx, t, dloss = make(M, V, k, DT[dt], torch.float32, seed=z0 + 8 * d0)
+    zb = torch.full((M * V + 8,), float("nan"), dtype=DT[dt], device="cuda")
+    db = torch.full((M * V + 8,), 7.0, dtype=DT[out], device="cuda")
+    zv, dv = (b[o:o + M * V].view(M, V) for b, o in ((zb, z0), (db, d0)))
+    zv.copy_(z)
+    idx2, t2 = (torch.cat([v.flatten()[:1], v.flatten()])[1:].view(M, k) for v in (idx, t))   # 4 bytes in
+    check_case(zv, idx2, t2, 1.0, dloss, DT[out], dlogits=dv)
+    assert torch.all(db[:d0] == 7.0) and torch.all(db[d0 + M * V:] == 7.0)
 
 
 @pytest.mark.gpu
