@@ -651,11 +651,11 @@ inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int32_t half_width(int32_t r) { return r <= 32 ? 32 : (int32_t)round_up(r, 64); }
 
 // Workspace, every piece 256-byte aligned:
-//   the lists; U, fp32 [M, r] (when the caller keeps none); U2 and dU2, 16-bit [M, 2R] (hi | lo of s U
+//   the lists; U2 and dU2, 16-bit [M, 2R] (hi | lo of s U
 //   and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
 //   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
 struct AdaptersWs {
-    size_t tok, n512, e512, n128, e128, n_grad, e_grad, u, u2, du2, part, b8, dy8, total;
+    size_t tok, n512, e512, n128, e128, n_grad, e_grad, u2, du2, part, b8, dy8, total;
     int32_t cap512, cap128, tiles64;
     int64_t tiles512;
 };
@@ -678,11 +678,10 @@ AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     w.e128 = piece((size_t)t128 * w.cap128 * kPartEntry * 4);
     w.n_grad = piece(n * 4);
     w.e_grad = piece((size_t)n * w.tiles64 * 16);
-    w.u = piece((size_t)M * r * 4);
     w.u2 = piece((size_t)M * 2 * R * 2);
     w.du2 = piece((size_t)M * 2 * R * 2);
     size_t part = (size_t)std::max(part_splits(M, K, r), part_splits(M, N, r)) * M * Rn * 4;
-    if (M <= kDecodeMaxM) part = std::max(part, decode_partial_bytes(N, K));
+    if (M <= kRowsMaxM) part = std::max(part, rows_workspace_bytes(M, N, K, r, n));
     w.part = piece(part);
     w.b8 = piece(r % 8 ? (size_t)n * N * round_up(r, 8) * 2 : 0);
     w.dy8 = piece(N % 8 ? (size_t)M * round_up(N, 8) * 2 : 0);
@@ -884,15 +883,13 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     float* partial = reinterpret_cast<float*>(ws + lw.part);
-    float* U = U_save ? U_save : reinterpret_cast<float*>(ws + lw.u);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
-    if (M <= kDecodeMaxM) {
-        DecodeArgs d{};
-        d.w = w; d.X = X; d.A = A_all; d.B = B_all; d.r = r; d.scale = 0.f; d.scales = scales; d.M = M; d.out = Y;
-        d.out_f32 = (y_dtype == QLORA_DTYPE_F32);
-        d.U = U; d.partial = partial; d.aidx = adapter_idx; d.n_adapters = n_adapters;
+    if (M <= kRowsMaxM) {
+        RowsArgs a{};
+        a.w = w; a.X = X; a.A = A_all; a.B = B_all; a.idx = adapter_idx; a.scales = scales; a.n_adapters = n_adapters;
+        a.r = r; a.M = M; a.out = Y; a.out_f32 = (y_dtype == QLORA_DTYPE_F32); a.U = U_save; a.workspace = ws + lw.part;
         TimerScope t(QLORA_TIMER_DECODE, s);
-        return launch_tc_decode(d, s);
+        return launch_rows(a, s);
     }
     const AdapterLists l = lists_at(ws, lw);
     void* U2 = ws + lw.u2;

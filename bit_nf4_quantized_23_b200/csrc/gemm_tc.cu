@@ -43,6 +43,7 @@
 #include "qlora_internal.cuh"
 #include "tc_ptx.cuh"
 #include "gemm_tc.cuh"
+#include "nf4_expand.cuh"
 
 namespace qlora {
 namespace {
@@ -70,101 +71,6 @@ struct Layout {
     static constexpr uint32_t kBytes = kAbort + 4;
     static constexpr uint32_t kAlloc = kBytes + 1024;      // slack for 1024-byte alignment
 };
-
-// prmt.b32 in its default mode: byte i of the result is source byte (s_i & 7)
-// of {y, x}; when bit 3 of the selector nibble s_i is set, that byte's sign bit
-// is replicated over all 8 bits.  (The __byte_perm intrinsic ignores bit 3, so
-// the sign-replicating selectors below need the instruction itself.)
-__device__ __forceinline__ uint32_t prmt(uint32_t x, uint32_t y, uint32_t s) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(s));
-    return r;
-}
-
-struct Lut {
-    uint32_t L[4], H[4];   // low / high bytes of the 16 bf16 entries, 4 entries per register
-};
-
-__device__ __forceinline__ void build_lut(Lut& t, float c1p, const NF4Tables& tb, bool f16) {
-    uint32_t P[8];   // entries 2j, 2j+1 rounded to the compute dtype (bf16 or fp16), packed
-    const float2 c2p = make_float2(c1p, c1p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 e = mul2_rn(make_float2(tb.q[2 * j], tb.q[2 * j + 1]), c2p);   // fp32(q * c1'), per element
-        P[j] = pack16x2_rn(e.x, e.y, f16);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        t.L[j] = prmt(P[2 * j], P[2 * j + 1], 0x6420);
-        t.H[j] = prmt(P[2 * j], P[2 * j + 1], 0x7531);
-    }
-}
-
-// 8 codes (4 packed bytes, element 2j in the high nibble of byte j) -> 8 bf16.
-// The nibbles of w run e1, e0, e3, e2, ... from the least significant end; the
-// table permutes keep that pair-swapped order and the final interleave undoes
-// it.  Bytes whose code is >= 8 take entries 8-15 (sign-replicated bit 3).
-__device__ __forceinline__ uint4 expand8(uint32_t w, const Lut& t) {
-    const uint32_t u = w << 4;             // bit 3 of the low nibble of each byte -> that byte's bit 7
-    const uint32_t wm = w & 0x77777777u;   // table index of every code; prmt reads selector bits 0-15
-    uint32_t o[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t sel = h == 0 ? wm : (wm >> 16);
-        const uint32_t mask = prmt(u, w, h == 0 ? 0xD9C8u : 0xFBEAu);
-        const uint32_t la = prmt(t.L[0], t.L[1], sel);
-        const uint32_t lb = prmt(t.L[2], t.L[3], sel);
-        const uint32_t ha = prmt(t.H[0], t.H[1], sel);
-        const uint32_t hb = prmt(t.H[2], t.H[3], sel);
-        const uint32_t lo = (la & ~mask) | (lb & mask);
-        const uint32_t hi = (ha & ~mask) | (hb & mask);
-        o[2 * h] = prmt(lo, hi, 0x4051);
-        o[2 * h + 1] = prmt(lo, hi, 0x6273);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Expand one NF4 block (64 weights of one W row) into one 128-byte swizzled
-// row of a B image.  code_lo/code_hi: the two 16-byte halves of its codes.
-__device__ __forceinline__ void expand_block_row(uint32_t row_addr, uint32_t row_in_atom, uint4 c0, uint4 c1,
-                                                 const Lut& t) {
-    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-    for (int c = 0; c < 8; ++c) st_shared_v4(row_addr + ((c ^ row_in_atom) << 4), expand8(w[c], t));
-}
-
-__device__ __forceinline__ void zero_row(uint32_t row_addr) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) st_shared_v4(row_addr + (c << 4), make_uint4(0, 0, 0, 0));
-}
-
-// The same row in a non-swizzled K-major image (rows 16 bytes apart, chunk c of
-// every row LBO bytes after chunk 0): the eight stores take immediate offsets from
-// one address, and a warp's 32 rows fill 512 contiguous bytes per chunk.
-template <uint32_t LBO>
-__device__ __forceinline__ void expand_block_row_kn(uint32_t row_addr, uint4 c0, uint4 c1, const Lut& t) {
-    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-    for (int c = 0; c < 8; ++c) st_shared_v4(row_addr + c * LBO, expand8(w[c], t));
-}
-
-template <uint32_t LBO>
-__device__ __forceinline__ void zero_row_kn(uint32_t row_addr) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) st_shared_v4(row_addr + c * LBO, make_uint4(0, 0, 0, 0));
-}
 
 // Output tile of CTA t: row tiles run fastest within groups of kRasterGroup of them, so the
 // CTAs resident at one time share a W strip (read from HBM once, then from L2) and keep the
@@ -1217,7 +1123,7 @@ constexpr int kFixSlotBatch = 8;
 __global__ void __launch_bounds__(128)
 decode_fixup(const float* __restrict__ partial, int64_t units, int64_t G, int S, int64_t M, int64_t N,
              const float* __restrict__ U, const uint16_t* __restrict__ B, int r, float scale, void* out, int out_f32,
-             const int32_t* __restrict__ aidx, int n_adapters, const float* __restrict__ scales, bool f16) {
+             const int32_t* __restrict__ aidx, int n_adapters, bool f16) {
     extern __shared__ float us[];                             // us[j * 4 + q] = U[m0 + q, j]
     __shared__ int32_t tok_adapter[kFixTokens];
     const int m0 = (int)blockIdx.y * kFixTokens;
@@ -1302,8 +1208,7 @@ decode_fixup(const float* __restrict__ partial, int64_t units, int64_t G, int S,
     for (int q = 0; q < kFixTokens; ++q) {
         if (q < nm) {
             const int64_t m = m0 + q;
-            const int a = tok_adapter[q];
-            const float y = __fmaf_rn(scales && a >= 0 ? __ldg(scales + a) : scale, lora[q], acc[q]);
+            const float y = __fmaf_rn(scale, lora[q], acc[q]);
             if (out_f32) static_cast<float*>(out)[m * N + n] = y;
             else static_cast<uint16_t*>(out)[m * N + n] = (uint16_t)to16_rn(y, f16);
         }
@@ -1342,6 +1247,18 @@ bool make_tmap_2d(CUtensorMap* map, bool bf16, const void* base, uint64_t inner,
               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_codes64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {inner};
+    const cuuint32_t box[2] = {64, 128};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
@@ -1528,7 +1445,7 @@ qlora_status launch_tc_decode(const DecodeArgs& a, cudaStream_t stream) {
                            (size_t)a.r * kFixTokens * sizeof(float), stream,
                            (const float*)a.partial, p.units, p.grid, (int)p.ksteps, a.M, N, (const float*)a.U,
                            static_cast<const uint16_t*>(a.B), a.r, a.scale, a.out, (int)a.out_f32, a.aidx,
-                           (int)a.n_adapters, a.scales, p.f16 != 0);
+                           (int)a.n_adapters, p.f16 != 0);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }

@@ -99,13 +99,31 @@ struct DecodeArgs {
     float* U;               // [M, r] fp32, written (X A^T)
     float* partial;         // decode_partial_bytes(N, K)
     const int32_t* aidx;    // multi-adapter: device [M] adapter of each token (-1: none); NULL: one adapter
-    const float* scales;    // multi-adapter: device [n_adapters] scale of each adapter, or NULL: `scale` for all
     int32_t n_adapters;     // multi-adapter: A is [n_adapters, r, K], B is [n_adapters, N, r]
 };
 
 constexpr int64_t kDecodeMaxM = 16;
 size_t decode_partial_bytes(int64_t N, int64_t K);
 qlora_status launch_tc_decode(const DecodeArgs& a, cudaStream_t stream);
+
+// Forward of up to 128 tokens with one adapter each (decode_adapters.cu).
+struct RowsArgs {
+    const qlora_nf4_weight* w;
+    const void* X;          // [M, K]
+    const void* A;          // [n_adapters, r, K]
+    const void* B;          // [n_adapters, N, r]
+    const int32_t* idx;     // [M]
+    const float* scales;    // [n_adapters]
+    int32_t n_adapters, r;
+    int64_t M;
+    void* out;
+    int32_t out_f32;
+    float* U;               // [M, r] fp32 or NULL
+    void* workspace;        // rows_workspace_bytes
+};
+constexpr int64_t kRowsMaxM = 128;
+size_t rows_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n_adapters);
+qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream);
 
 // LoRA-side GEMM (gemm_lora_tc.cu): partial[split][rows][R] = sum over the
 // split's share of the reduction of A-operand rows times B-operand rows.
@@ -141,6 +159,8 @@ qlora_status launch_lora_gemm(const LoraGemmArgs& a, cudaStream_t stream);
 int lora_splits(int64_t rows, int ksteps_total, int R, bool mn_major);
 size_t lora_partial_bytes(int64_t rows, int64_t red, int R, bool mn_major);
 
+// Map of packed codes, rows of `inner` bytes, boxes of 128 rows x 64 bytes (two blocks), 64-byte swizzle.
+bool make_tmap_codes64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer);
 // Rank-3 map of a 16-bit [d2, d1, d0] array with contiguous rows, 128-byte swizzle, boxes one deep.
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
                   uint32_t box1);

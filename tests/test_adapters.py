@@ -178,6 +178,24 @@ def test_forward_and_backward(M, N, K, r, n, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n", [(2, 5, 64, 3, 2), (31, 4200, 192, 16, 9), (33, 1000, 2112, 48, 8), (64, 131, 1024, 7, 64),
+                                       (65, 2000, 320, 200, 3), (96, 40, 4096, 130, 40), (113, 20000, 128, 64, 2),
+                                       (128, 700, 704, 256, 128)])
+def test_few_tokens(M, N, K, r, n):
+    """Up to 128 tokens take kernels of their own: odd numbers of 64-wide blocks, ranks that are no power
+    of two, an adapter per token, one tile for all CTAs and many tiles each."""
+    c = Case(M, N, K, r, n, "mixed", seed=4)
+    ref, tol = c.reference()
+    for out in (F32, BF16):
+        Y, U = c.fwd(y_dtype=out)
+        close("U", U, ref["U"], tol["U"])
+        close("Y", Y, ref["Y"], tol["Y"])
+    Y2, none = c.fwd(save_U=False)
+    assert none is None and torch.equal(Y, Y2)
+    assert q4.qlora_read_device_errors(clear=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", ["one", "none"])
 @pytest.mark.parametrize("M,N,K,r,n", [(5, 130, 128, 8, 2), (90, 200, 256, 16, 3), (600, 264, 192, 40, 2)])
 def test_a_single_adapter_and_none_at_all(M, N, K, r, n, rows):
