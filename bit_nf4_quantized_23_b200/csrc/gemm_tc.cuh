@@ -159,8 +159,8 @@ qlora_status launch_lora_gemm(const LoraGemmArgs& a, cudaStream_t stream);
 int lora_splits(int64_t rows, int ksteps_total, int R, bool mn_major);
 size_t lora_partial_bytes(int64_t rows, int64_t red, int R, bool mn_major);
 
-// Map of packed codes, rows of `inner` bytes, boxes of 128 rows x 64 bytes (two blocks), 64-byte swizzle.
-bool make_tmap_codes64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer);
+// Map of packed codes, rows of `inner` bytes, boxes of 256 rows x 32 bytes (one block), 32-byte swizzle.
+bool make_tmap_codes32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer);
 // Rank-3 map of a 16-bit [d2, d1, d0] array with contiguous rows, 128-byte swizzle, boxes one deep.
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
                   uint32_t box1);
