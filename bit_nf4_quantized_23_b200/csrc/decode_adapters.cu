@@ -412,12 +412,15 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     }
 }
 
-// Y[m, n] = the sum of the partial tiles of n / 256 in CTA order + s_a sum_j U[m, j] B_a[n, j] (fp32),
-// rounded to the output type.  CTA (x, y): columns 128 x .. 128 x + 127, tokens 16 y .. 16 y + 15.  U is
-// summed from its own partial tiles; the CTAs of x = 0 also store it.  A thread keeps 64 ranks of one
-// B row in registers while the tokens that follow each other use the same adapter.
-constexpr int kFixTokens = 16;
-constexpr int kFixRanks = 64;
+// Y[m, n] = the sum of the partial tiles of n / 256 in CTA order + sum_j (s_a U[m, j]) B_a[n, j] (fp32),
+// rounded to the output type.  CTA (tile, y): the tile's 256 columns (two per thread), tokens 8 y .. 8 y + 7.
+// The kernel is a chain of memory latencies, so each link has all its loads in flight: the B rows of the
+// CTA's tokens come by cp.async, 64 KiB at a time, while U is summed from its own partial tiles and the
+// base product from its slots.  Neighbouring tokens of one request are a run and share B.  A thread
+// reads only the B rows that it copied itself.
+constexpr int kFixThreads = 128;
+constexpr int kFixTokens = 8;
+constexpr int kFixChunks = 16;                    // 16-byte chunks (8 ranks) of B per column and pass, over all runs
 
 struct FixParams {
     const float* partial;
@@ -433,10 +436,17 @@ struct FixParams {
     int32_t out_f32, f16;
 };
 
-__global__ void __launch_bounds__(128)
+__host__ __device__ inline uint32_t fixup_smem(int r) {
+    return kFixChunks * 256 * 16 + kFixTokens * (uint32_t)((r + 7) / 8 * 8) * 4;
+}
+
+__global__ void __launch_bounds__(kFixThreads)
 rows_fixup(FixParams p) {
-    extern __shared__ float us[];                             // us[q * pitch + j] = U[m0 + q, j], zeros for j >= r
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4* bs = reinterpret_cast<uint4*>(smem);               // bs[(run * chunks + c) * 256 + column]
+    float* us = reinterpret_cast<float*>(smem + kFixChunks * 256 * 16);   // us[q * pitch + j] = s_a U[m0 + q, j]
     __shared__ int32_t tok_place[kFixTokens], tok_adapter[kFixTokens];
+    __shared__ int32_t run_adapter[kFixTokens], run_end[kFixTokens], runs_of;
     __shared__ int2 span[129];                                // first and last CTA of each tile of A_all rows; [128]: this tile's
     const int tid = threadIdx.x, m0 = (int)blockIdx.y * kFixTokens, nm = min(p.M - m0, kFixTokens);
     grid_dependency_wait();                                   // partial tiles are complete
@@ -444,112 +454,157 @@ rows_fixup(FixParams p) {
     const int u_tiles = (p.meta[0] + per_tile - 1) / per_tile;
     const int64_t units = (int64_t)(u_tiles + p.w_tiles) * p.steps;
     const int64_t slot_floats = (int64_t)p.nt * 256;
-    auto cta_of = [&](int64_t u) {                            // the CTA whose range holds unit u
-        int64_t b = u * p.G / units;
-        while (b + 1 < p.G && range_begin(b + 1, units, p.G) <= u) ++b;
-        while (b > 0 && range_begin(b, units, p.G) > u) --b;
-        return (int)b;
-    };
-    const int tile = u_tiles + (int)(blockIdx.x >> 1);
+    const int tile = u_tiles + (int)blockIdx.x;
+    // the CTA whose range holds unit u: the largest b with b units / G <= u, that is b units < (u + 1) G
+    auto cta_of = [&](int64_t u) { return (int)(((u + 1) * p.G - 1) / units); };
     auto span_of = [&](int t) {
         return make_int2(cta_of((int64_t)t * p.steps), cta_of((int64_t)t * p.steps + p.steps - 1));
     };
     if (tid < u_tiles) span[tid] = span_of(tid);
-    if (tid == 127) span[128] = span_of(tile);
+    if (tid == kFixThreads - 1) span[128] = span_of(tile);
     if (tid < kFixTokens) {
         const int place = tid < nm ? p.meta[1 + m0 + tid] : -1;
         tok_place[tid] = place;
         tok_adapter[tid] = place >= 0 ? p.idx[m0 + tid] : -1;
     }
     __syncthreads();
-    const int rpad = (p.r + 3) & ~3, pitch = rpad + 4;
-    for (int i = tid; i < kFixTokens * rpad; i += 128) {
-        const int q = i / rpad, j = i - q * rpad;
-        float v = 0.f;
-        if (tok_place[q] >= 0 && j < p.r) {
-            const int t = tok_place[q] / per_tile, row = (tok_place[q] - t * per_tile) * p.rp + j;
-            const int2 sp = span[t];
-            const float* src = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)(m0 + q) * 256 + row;
-            for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) v = __fadd_rn(v, *src);
+    if (tid == 0) {
+        int runs = 0, have = -1;
+        for (int q = 0; q < kFixTokens; ++q) {
+            const int a = tok_adapter[q];
+            if (a >= 0 && a != have) run_adapter[runs++] = a;
+            if (a >= 0) run_end[runs - 1] = q + 1;
+            have = a;
         }
-        us[q * pitch + j] = v;
-        if (p.U && blockIdx.x == 0 && q < nm && j < p.r) p.U[(int64_t)(m0 + q) * p.r + j] = v;
-    }
-    // this thread's column of the base product, summed in CTA order
-    const int64_t n = (int64_t)blockIdx.x * 128 + tid;
-    const bool in = n < p.N;
-    float acc[kFixTokens];
-#pragma unroll
-    for (int q = 0; q < kFixTokens; ++q) acc[q] = 0.f;
-    const int2 sp = span[128];
-    const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)m0 * 256 + (blockIdx.x & 1) * 128 + tid;
-    for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
-        float v[kFixTokens];
-#pragma unroll
-        for (int q = 0; q < kFixTokens; ++q) v[q] = q < nm ? src[q * 256] : 0.f;
-#pragma unroll
-        for (int q = 0; q < kFixTokens; ++q) acc[q] = __fadd_rn(acc[q], v[q]);
+        runs_of = runs;
     }
     __syncthreads();
-    if (!in) return;
-    const bool f16 = p.f16 != 0, vec = (p.r & 7) == 0;
-    float lora[kFixTokens];
+    const int runs = runs_of, all_chunks = (p.r + 7) / 8, pitch = all_chunks * 8;
+    const int pass_chunks = runs > 0 ? min(all_chunks, kFixChunks / runs) : 0;
+    const int64_t n0 = (int64_t)blockIdx.x * 256 + tid;
+    auto fetch = [&](int c0) {                                // B chunks c0 .. of every run, this thread's two columns
+        const int nc = min(pass_chunks, all_chunks - c0);
+        for (int run = 0; run < runs; ++run) {
 #pragma unroll
-    for (int q = 0; q < kFixTokens; ++q) lora[q] = 0.f;
-    for (int j0 = 0; j0 < p.r; j0 += kFixRanks) {
-        float2 bv[kFixRanks / 2];
-        const int nr = min(p.r - j0, kFixRanks);
-        int have = -1;
-#pragma unroll 1
-        for (int q = 0; q < nm; ++q) {
-            const int a = tok_adapter[q];
-            if (a < 0) continue;
-            if (a != have) {                                  // tokens of one request follow each other
-                have = a;
-                const uint16_t* br = p.B + ((int64_t)a * p.N + n) * p.r + j0;
-                if (vec) {
-                    uint4 w[kFixRanks / 8];
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + 128 * h;
+                if (n >= p.N) continue;
+                const uint16_t* src = p.B + ((int64_t)run_adapter[run] * p.N + n) * p.r + c0 * 8;
+                uint4* dst = bs + run * pass_chunks * 256 + tid + 128 * h;
+                if ((p.r & 7) == 0) {
+                    for (int c = 0; c < nc; ++c)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst + c * 256)),
+                                     "l"(src + 8 * c) : "memory");
+                } else {                                      // rows of B start anywhere
+                    for (int c = 0; c < nc; ++c) {
+                        uint32_t v[8];
 #pragma unroll
-                    for (int c = 0; c < kFixRanks / 8; ++c)
-                        w[c] = 8 * c < nr ? __ldg(reinterpret_cast<const uint4*>(br) + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < kFixRanks / 8; ++c) {
-                        const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            bv[4 * c + e] = make_float2(from16(v[e] & 0xFFFFu, f16), from16(v[e] >> 16, f16));
+                        for (int e = 0; e < 8; ++e) v[e] = (c0 + c) * 8 + e < p.r ? src[8 * c + e] : 0u;
+                        dst[c * 256] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kFixRanks / 2; ++e)
-                        bv[e] = make_float2(2 * e < nr ? from16(br[2 * e], f16) : 0.f,
-                                            2 * e + 1 < nr ? from16(br[2 * e + 1], f16) : 0.f);
                 }
             }
-            // even and odd ranks in the two halves of packed multiply-adds
-            const float4* u4 = reinterpret_cast<const float4*>(us + q * pitch + j0);
-            float2 d = make_float2(0.f, 0.f);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(0);
+
+    for (int i0 = tid; i0 < kFixTokens * pitch; i0 += 4 * kFixThreads) {
+        const float* src[4];
+        int left[4], most = 0;
+        float v[4], sc[4];
 #pragma unroll
-            for (int c = 0; c < kFixRanks / 4; ++c) {
-                if (4 * c >= nr) break;
-                const float4 u = u4[c];
-                d = fma2_rn(make_float2(u.x, u.y), bv[2 * c], d);
-                d = fma2_rn(make_float2(u.z, u.w), bv[2 * c + 1], d);
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e * kFixThreads, q = i / pitch, j = i - q * pitch;
+            v[e] = 0.f;
+            left[e] = 0;
+            if (i < kFixTokens * pitch && j < p.r && tok_place[q] >= 0) {
+                const int t = tok_place[q] / per_tile, row = (tok_place[q] - t * per_tile) * p.rp + j;
+                const int2 sp = span[t];
+                src[e] = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)(m0 + q) * 256 + row;
+                left[e] = sp.y - sp.x + 1;
+                sc[e] = __ldg(p.scales + tok_adapter[q]);
+                most = max(most, left[e]);
             }
-            const float sum = __fadd_rn(d.x, d.y);
+        }
+        for (int b = 0; b < most; ++b) {
+            float x[4];
 #pragma unroll
-            for (int e = 0; e < kFixTokens; ++e)
-                if (e == q) lora[e] = __fadd_rn(lora[e], sum);
+            for (int e = 0; e < 4; ++e) x[e] = b < left[e] ? src[e][b * slot_floats] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(v[e], x[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e * kFixThreads, q = i / pitch, j = i - q * pitch;
+            if (i >= kFixTokens * pitch) continue;
+            us[i] = left[e] > 0 ? __fmul_rn(sc[e], v[e]) : 0.f;
+            if (p.U && blockIdx.x == 0 && q < nm && j < p.r) p.U[(int64_t)(m0 + q) * p.r + j] = v[e];
+        }
+    }
+
+    float2 acc[kFixTokens][2];                                // .x the base product, then the even ranks' terms; .y the odd ones'
+#pragma unroll
+    for (int q = 0; q < kFixTokens; ++q) acc[q][0] = acc[q][1] = make_float2(0.f, 0.f);
+    const int2 sp = span[128];
+    const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)m0 * 256 + tid;
+    for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
+        float v[kFixTokens][2];
+#pragma unroll
+        for (int q = 0; q < kFixTokens; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[q][h] = q < nm ? src[q * 256 + 128 * h] : 0.f;
+#pragma unroll
+        for (int q = 0; q < kFixTokens; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) acc[q][h].x = __fadd_rn(acc[q][h].x, v[q][h]);
+    }
+    __syncthreads();                                          // us
+
+    const bool f16 = p.f16 != 0;
+    for (int c0 = 0; c0 < all_chunks && runs > 0; c0 += pass_chunks) {
+        if (c0 > 0) fetch(c0);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const int nc = min(pass_chunks, all_chunks - c0);
+        for (int run = 0; run < runs; ++run) {
+            const int a = run_adapter[run], qe = run_end[run];
+            for (int c = 0; c < nc; ++c) {
+                float2 bv[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 w = bs[(run * pass_chunks + c) * 256 + tid + 128 * h];
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bv[h][e] = make_float2(from16(x[e] & 0xFFFFu, f16), from16(x[e] >> 16, f16));
+                }
+#pragma unroll
+                for (int q = 0; q < kFixTokens; ++q) {
+                    // a run's tokens: those before its end that use its adapter after the run before it
+                    if (q >= qe || tok_adapter[q] != a || (run > 0 && q < run_end[run - 1])) continue;
+                    const float4* u4 = reinterpret_cast<const float4*>(us + q * pitch + (c0 + c) * 8);
+                    const float4 u0 = u4[0], u1 = u4[1];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        acc[q][h] = fma2_rn(make_float2(u0.x, u0.y), bv[h][0], acc[q][h]);
+                        acc[q][h] = fma2_rn(make_float2(u0.z, u0.w), bv[h][1], acc[q][h]);
+                        acc[q][h] = fma2_rn(make_float2(u1.x, u1.y), bv[h][2], acc[q][h]);
+                        acc[q][h] = fma2_rn(make_float2(u1.z, u1.w), bv[h][3], acc[q][h]);
+                    }
+                }
+            }
         }
     }
 #pragma unroll
     for (int q = 0; q < kFixTokens; ++q) {
         if (q >= nm) break;
-        const int a = tok_adapter[q];
-        const float y = a >= 0 ? __fmaf_rn(__ldg(p.scales + a), lora[q], acc[q]) : acc[q];
-        const int64_t at = (int64_t)(m0 + q) * p.N + n;
-        if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)to16_rn(y, f16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = n0 + 128 * h, at = (int64_t)(m0 + q) * p.N + n;
+            if (n >= p.N) continue;
+            const float y = __fadd_rn(acc[q][h].x, acc[q][h].y);
+            if (p.out_f32) static_cast<float*>(p.out)[at] = y;
+            else static_cast<uint16_t*>(p.out)[at] = (uint16_t)to16_rn(y, f16);
+        }
     }
 }
 
@@ -613,8 +668,14 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     f.B = static_cast<const uint16_t*>(a.B); f.U = a.U; f.out = a.out; f.N = N;
     f.M = p.M; f.r = p.r; f.rp = p.rp; f.steps = p.steps; f.w_tiles = p.w_tiles; f.G = (int32_t)G; f.nt = p.nt;
     f.out_f32 = a.out_f32; f.f16 = p.f16;
-    const dim3 grid((unsigned)((N + 127) / 128), (unsigned)((a.M + kFixTokens - 1) / kFixTokens));
-    (void)launch_dependent(rows_fixup, grid, dim3(128), (size_t)(a.r + 8) * kFixTokens * sizeof(float), stream, f);
+    const dim3 grid((unsigned)p.w_tiles, (unsigned)((a.M + kFixTokens - 1) / kFixTokens));
+    static bool fix_configured = false;
+    if (!fix_configured) {
+        if (cudaFuncSetAttribute(rows_fixup, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fixup_smem(256)) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        fix_configured = true;
+    }
+    (void)launch_dependent(rows_fixup, grid, dim3(kFixThreads), fixup_smem(a.r), stream, f);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
