@@ -151,8 +151,11 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     __syncthreads();
     int first = tid;
     if (tid < 128) {
-        for (int j = tid - 1; j >= 0; --j)
-            if (ids[j] == a) first = j;
+        for (int j = (min(tid, p.M) - 1) & ~3; j >= 0; j -= 4) {   // ids past the batch are -1
+            const int4 v = *reinterpret_cast<const int4*>(ids + j);
+            const int f = v.x == a ? j : v.y == a ? j + 1 : v.z == a ? j + 2 : v.w == a ? j + 3 : 128;
+            first = min(first, f);
+        }
         const uint32_t b = __ballot_sync(0xffffffffu, a >= 0 && first == tid);
         if (lane == 0) ballots[warp] = b;
     }
@@ -413,14 +416,14 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
 }
 
 // Y[m, n] = the sum of the partial tiles of n / 256 in CTA order + sum_j (s_a U[m, j]) B_a[n, j] (fp32),
-// rounded to the output type.  CTA (tile, y): the tile's 256 columns (two per thread), tokens 8 y .. 8 y + 7.
-// The kernel is a chain of memory latencies, so each link has all its loads in flight: the B rows of the
-// CTA's tokens come by cp.async, 64 KiB at a time, while U is summed from its own partial tiles and the
-// base product from its slots.  Neighbouring tokens of one request are a run and share B.  A thread
-// reads only the B rows that it copied itself.
-constexpr int kFixThreads = 128;
-constexpr int kFixTokens = 8;
-constexpr int kFixChunks = 16;                    // 16-byte chunks (8 ranks) of B per column and pass, over all runs
+// rounded to the output type.  CTA (tile, y): the tile's 256 columns and the y-th 8 or 16 tokens; a thread has
+// one column and half of the tokens.  The kernel is a chain of memory latencies, so each link has all its
+// loads in flight: the B rows of the CTA's tokens come by cp.async, 32 KiB at a time, while U is summed
+// from its own partial tiles and the base product from its slots.  Neighbouring tokens of one request
+// are a run and share B.
+constexpr int kFixThreads = 512;
+constexpr int kFixLoads = 16;                     // loads of partial sums that a thread has in flight together
+constexpr int kFixChunks = 8;                     // 16-byte chunks (8 ranks) of B per column and pass, over all runs
 
 struct FixParams {
     const float* partial;
@@ -436,19 +439,23 @@ struct FixParams {
     int32_t out_f32, f16;
 };
 
-__host__ __device__ inline uint32_t fixup_smem(int r) {
-    return kFixChunks * 256 * 16 + kFixTokens * (uint32_t)((r + 7) / 8 * 8) * 4;
+__host__ __device__ inline uint32_t fixup_smem(int r, int tokens) {
+    return kFixChunks * 256 * 16 + (uint32_t)tokens * (uint32_t)((r + 7) / 8 * 8) * 4;
 }
 
-__global__ void __launch_bounds__(kFixThreads)
+// kFixOwn: tokens of a thread; a CTA has twice as many.
+template <int kFixOwn>
+__global__ void __launch_bounds__(kFixThreads, 2)
 rows_fixup(FixParams p) {
+    constexpr int kFixTokens = 2 * kFixOwn, kFixSlots = kFixLoads / kFixOwn;
     extern __shared__ __align__(16) uint8_t smem[];
-    uint4* bs = reinterpret_cast<uint4*>(smem);               // bs[(run * chunks + c) * 256 + column]
+    uint4* bs = reinterpret_cast<uint4*>(smem);               // bs[(run * pass_chunks + c) * 256 + column]
     float* us = reinterpret_cast<float*>(smem + kFixChunks * 256 * 16);   // us[q * pitch + j] = s_a U[m0 + q, j]
-    __shared__ int32_t tok_place[kFixTokens], tok_adapter[kFixTokens];
-    __shared__ int32_t run_adapter[kFixTokens], run_end[kFixTokens], runs_of;
+    __shared__ int32_t tok_place[kFixTokens], tok_adapter[kFixTokens], tok_run[kFixTokens], run_adapter[kFixTokens];
+    __shared__ int32_t runs_of;
     __shared__ int2 span[129];                                // first and last CTA of each tile of A_all rows; [128]: this tile's
-    const int tid = threadIdx.x, m0 = (int)blockIdx.y * kFixTokens, nm = min(p.M - m0, kFixTokens);
+    const int tid = threadIdx.x, col = tid & 255, q0 = (tid >> 8) * kFixOwn;
+    const int m0 = (int)blockIdx.y * kFixTokens, nm = min(p.M - m0, kFixTokens);
     grid_dependency_wait();                                   // partial tiles are complete
     const int per_tile = adapters_per_tile(p.rp);
     const int u_tiles = (p.meta[0] + per_tile - 1) / per_tile;
@@ -460,157 +467,150 @@ rows_fixup(FixParams p) {
     auto span_of = [&](int t) {
         return make_int2(cta_of((int64_t)t * p.steps), cta_of((int64_t)t * p.steps + p.steps - 1));
     };
-    if (tid < u_tiles) span[tid] = span_of(tid);
-    if (tid == kFixThreads - 1) span[128] = span_of(tile);
-    if (tid < kFixTokens) {
+    if (tid >= 256 && tid - 256 < u_tiles) span[tid - 256] = span_of(tid - 256);
+    if (tid == 128) span[128] = span_of(tile);
+    if (tid < 32) {                                           // tokens, and the runs of equal adapters among them
         const int place = tid < nm ? p.meta[1 + m0 + tid] : -1;
-        tok_place[tid] = place;
-        tok_adapter[tid] = place >= 0 ? p.idx[m0 + tid] : -1;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int runs = 0, have = -1;
-        for (int q = 0; q < kFixTokens; ++q) {
-            const int a = tok_adapter[q];
-            if (a >= 0 && a != have) run_adapter[runs++] = a;
-            if (a >= 0) run_end[runs - 1] = q + 1;
-            have = a;
+        const int a = place >= 0 ? p.idx[m0 + tid] : -1;
+        const int before = __shfl_up_sync(0xffffffffu, a, 1);
+        const uint32_t starts = __ballot_sync(0xffffffffu, a >= 0 && (tid == 0 || a != before));
+        const int run = __popc(starts & (0xffffffffu >> (31 - tid))) - 1;
+        if (tid < kFixTokens) {
+            tok_place[tid] = place;
+            tok_adapter[tid] = a;
+            tok_run[tid] = a >= 0 ? run : -1;
+            if (starts >> tid & 1u) run_adapter[run] = a;
         }
-        runs_of = runs;
+        if (tid == 0) runs_of = __popc(starts);
     }
     __syncthreads();
     const int runs = runs_of, all_chunks = (p.r + 7) / 8, pitch = all_chunks * 8;
-    const int pass_chunks = runs > 0 ? min(all_chunks, kFixChunks / runs) : 0;
-    const int64_t n0 = (int64_t)blockIdx.x * 256 + tid;
-    auto fetch = [&](int c0) {                                // B chunks c0 .. of every run, this thread's two columns
-        const int nc = min(pass_chunks, all_chunks - c0);
-        for (int run = 0; run < runs; ++run) {
+    // runs and chunks of B that are in shared memory together
+    const int pass_runs = min(runs, kFixChunks), pass_chunks = runs > 0 ? min(all_chunks, kFixChunks / pass_runs) : 0;
+    const int64_t n = (int64_t)blockIdx.x * 256 + col;
+    const bool in = n < p.N;
+    auto fetch = [&](int r0, int c0) {                        // B chunks c0 .. of runs r0 ..
+        const int nr = min(pass_runs, runs - r0), nc = min(pass_chunks, all_chunks - c0);
+        for (int e = tid >> 8; e < nr * nc && in; e += 2) {
+            const int run = e / nc, c = e - run * nc;
+            const uint16_t* src = p.B + ((int64_t)run_adapter[r0 + run] * p.N + n) * p.r + (c0 + c) * 8;
+            uint4* dst = bs + (run * pass_chunks + c) * 256 + col;
+            if ((p.r & 7) == 0) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
+            } else {                                          // rows of B start anywhere
+                uint32_t v[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t n = n0 + 128 * h;
-                if (n >= p.N) continue;
-                const uint16_t* src = p.B + ((int64_t)run_adapter[run] * p.N + n) * p.r + c0 * 8;
-                uint4* dst = bs + run * pass_chunks * 256 + tid + 128 * h;
-                if ((p.r & 7) == 0) {
-                    for (int c = 0; c < nc; ++c)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst + c * 256)),
-                                     "l"(src + 8 * c) : "memory");
-                } else {                                      // rows of B start anywhere
-                    for (int c = 0; c < nc; ++c) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = (c0 + c) * 8 + e < p.r ? src[8 * c + e] : 0u;
-                        dst[c * 256] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                    }
-                }
+                for (int i = 0; i < 8; ++i) v[i] = (c0 + c) * 8 + i < p.r ? src[i] : 0u;
+                *dst = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0);
+    fetch(0, 0);
 
-    for (int i0 = tid; i0 < kFixTokens * pitch; i0 += 4 * kFixThreads) {
-        const float* src[4];
-        int left[4], most = 0;
-        float v[4], sc[4];
+    // the base product: .x starts with it and takes the even ranks' terms, .y the odd ones'
+    float2 acc[kFixOwn];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + e * kFixThreads, q = i / pitch, j = i - q * pitch;
-            v[e] = 0.f;
-            left[e] = 0;
-            if (i < kFixTokens * pitch && j < p.r && tok_place[q] >= 0) {
-                const int t = tok_place[q] / per_tile, row = (tok_place[q] - t * per_tile) * p.rp + j;
-                const int2 sp = span[t];
-                src[e] = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)(m0 + q) * 256 + row;
-                left[e] = sp.y - sp.x + 1;
-                sc[e] = __ldg(p.scales + tok_adapter[q]);
-                most = max(most, left[e]);
+    for (int q = 0; q < kFixOwn; ++q) acc[q] = make_float2(0.f, 0.f);
+    {
+        const int2 sp = span[128];
+        const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)(m0 + q0) * 256 + col;
+        for (int b = sp.x; b <= sp.y; b += kFixSlots, src += kFixSlots * slot_floats) {
+            float v[kFixSlots][kFixOwn];
+#pragma unroll
+            for (int e = 0; e < kFixSlots; ++e)
+#pragma unroll
+                for (int q = 0; q < kFixOwn; ++q)
+                    v[e][q] = q0 + q < nm && b + e <= sp.y ? src[e * slot_floats + q * 256] : 0.f;
+#pragma unroll
+            for (int e = 0; e < kFixSlots; ++e)
+#pragma unroll
+                for (int q = 0; q < kFixOwn; ++q) acc[q].x = __fadd_rn(acc[q].x, v[e][q]);
+        }
+    }
+    for (int i = tid; i < kFixTokens * pitch; i += kFixThreads) {
+        const int q = i / pitch, j = i - q * pitch;
+        float v = 0.f, sc = 0.f;
+        if (j < p.r && tok_place[q] >= 0) {
+            sc = __ldg(p.scales + tok_adapter[q]);
+            const int t = tok_place[q] / per_tile, row = (tok_place[q] - t * per_tile) * p.rp + j;
+            const int2 sp = span[t];
+            const float* src = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)(m0 + q) * 256 + row;
+            for (int b = sp.x; b <= sp.y; b += 8, src += 8 * slot_floats) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = b + e <= sp.y ? src[e * slot_floats] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v = __fadd_rn(v, x[e]);
             }
         }
-        for (int b = 0; b < most; ++b) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = b < left[e] ? src[e][b * slot_floats] : 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(v[e], x[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + e * kFixThreads, q = i / pitch, j = i - q * pitch;
-            if (i >= kFixTokens * pitch) continue;
-            us[i] = left[e] > 0 ? __fmul_rn(sc[e], v[e]) : 0.f;
-            if (p.U && blockIdx.x == 0 && q < nm && j < p.r) p.U[(int64_t)(m0 + q) * p.r + j] = v[e];
-        }
+        us[i] = __fmul_rn(sc, v);
+        if (p.U && blockIdx.x == 0 && q < nm && j < p.r) p.U[(int64_t)(m0 + q) * p.r + j] = v;
     }
-
-    float2 acc[kFixTokens][2];                                // .x the base product, then the even ranks' terms; .y the odd ones'
-#pragma unroll
-    for (int q = 0; q < kFixTokens; ++q) acc[q][0] = acc[q][1] = make_float2(0.f, 0.f);
-    const int2 sp = span[128];
-    const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)m0 * 256 + tid;
-    for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
-        float v[kFixTokens][2];
-#pragma unroll
-        for (int q = 0; q < kFixTokens; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v[q][h] = q < nm ? src[q * 256 + 128 * h] : 0.f;
-#pragma unroll
-        for (int q = 0; q < kFixTokens; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) acc[q][h].x = __fadd_rn(acc[q][h].x, v[q][h]);
-    }
-    __syncthreads();                                          // us
 
     const bool f16 = p.f16 != 0;
-    for (int c0 = 0; c0 < all_chunks && runs > 0; c0 += pass_chunks) {
-        if (c0 > 0) fetch(c0);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        const int nc = min(pass_chunks, all_chunks - c0);
-        for (int run = 0; run < runs; ++run) {
-            const int a = run_adapter[run], qe = run_end[run];
+    for (int r0 = 0; r0 < runs; r0 += pass_runs) {
+        for (int c0 = 0; c0 < all_chunks; c0 += pass_chunks) {
+            if (r0 > 0 || c0 > 0) {
+                __syncthreads();                              // the last pass has been read
+                fetch(r0, c0);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();                                  // us and every thread's copies
+            const int nc = min(pass_chunks, all_chunks - c0);
             for (int c = 0; c < nc; ++c) {
-                float2 bv[2][4];
+                int have = -1;
+                float2 bv[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 w = bs[(run * pass_chunks + c) * 256 + tid + 128 * h];
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                for (int q = 0; q < kFixOwn; ++q) {
+                    const int run = tok_run[q0 + q] - r0;
+                    if (run < 0 || run >= pass_runs) continue;
+                    if (run != have) {
+                        have = run;
+                        const uint4 w = bs[(run * pass_chunks + c) * 256 + col];
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) bv[h][e] = make_float2(from16(x[e] & 0xFFFFu, f16), from16(x[e] >> 16, f16));
-                }
-#pragma unroll
-                for (int q = 0; q < kFixTokens; ++q) {
-                    // a run's tokens: those before its end that use its adapter after the run before it
-                    if (q >= qe || tok_adapter[q] != a || (run > 0 && q < run_end[run - 1])) continue;
-                    const float4* u4 = reinterpret_cast<const float4*>(us + q * pitch + (c0 + c) * 8);
-                    const float4 u0 = u4[0], u1 = u4[1];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        acc[q][h] = fma2_rn(make_float2(u0.x, u0.y), bv[h][0], acc[q][h]);
-                        acc[q][h] = fma2_rn(make_float2(u0.z, u0.w), bv[h][1], acc[q][h]);
-                        acc[q][h] = fma2_rn(make_float2(u1.x, u1.y), bv[h][2], acc[q][h]);
-                        acc[q][h] = fma2_rn(make_float2(u1.z, u1.w), bv[h][3], acc[q][h]);
+                        for (int e = 0; e < 4; ++e)
+                            bv[e] = make_float2(from16(x[e] & 0xFFFFu, f16), from16(x[e] >> 16, f16));
                     }
+                    const float4* u4 = reinterpret_cast<const float4*>(us + (q0 + q) * pitch + (c0 + c) * 8);
+                    const float4 u0 = u4[0], u1 = u4[1];
+                    acc[q] = fma2_rn(make_float2(u0.x, u0.y), bv[0], acc[q]);
+                    acc[q] = fma2_rn(make_float2(u0.z, u0.w), bv[1], acc[q]);
+                    acc[q] = fma2_rn(make_float2(u1.x, u1.y), bv[2], acc[q]);
+                    acc[q] = fma2_rn(make_float2(u1.z, u1.w), bv[3], acc[q]);
                 }
             }
         }
     }
+    if (!in) return;
 #pragma unroll
-    for (int q = 0; q < kFixTokens; ++q) {
-        if (q >= nm) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t n = n0 + 128 * h, at = (int64_t)(m0 + q) * p.N + n;
-            if (n >= p.N) continue;
-            const float y = __fadd_rn(acc[q][h].x, acc[q][h].y);
-            if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-            else static_cast<uint16_t*>(p.out)[at] = (uint16_t)to16_rn(y, f16);
-        }
+    for (int q = 0; q < kFixOwn; ++q) {
+        if (q0 + q >= nm) break;
+        const int64_t at = (int64_t)(m0 + q0 + q) * p.N + n;
+        const float y = __fadd_rn(acc[q].x, acc[q].y);
+        if (p.out_f32) static_cast<float*>(p.out)[at] = y;
+        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)to16_rn(y, f16);
     }
 }
 
 // ---------------------------------------------------------------------------- host
 
 inline int32_t adapter_rows(int32_t r) { return (r + 7) / 8 * 8; }
+
+template <int OWN>
+qlora_status launch_fixup(const FixParams& f, cudaStream_t stream) {
+    static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
+    if (!configured) {
+        if (cudaFuncSetAttribute(rows_fixup<OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)fixup_smem(256, 2 * OWN)) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        configured = true;
+    }
+    const dim3 grid((unsigned)f.w_tiles, (unsigned)((f.M + 2 * OWN - 1) / (2 * OWN)));
+    (void)launch_dependent(rows_fixup<OWN>, grid, dim3(kFixThreads), fixup_smem(f.r, 2 * OWN), stream, f);
+    QLORA_CHECK_LAUNCH();
+    return QLORA_OK;
+}
 
 inline uint32_t token_tile(int64_t M) { return (uint32_t)((M + 7) / 8 * 8); }
 
@@ -668,15 +668,9 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     f.B = static_cast<const uint16_t*>(a.B); f.U = a.U; f.out = a.out; f.N = N;
     f.M = p.M; f.r = p.r; f.rp = p.rp; f.steps = p.steps; f.w_tiles = p.w_tiles; f.G = (int32_t)G; f.nt = p.nt;
     f.out_f32 = a.out_f32; f.f16 = p.f16;
-    const dim3 grid((unsigned)p.w_tiles, (unsigned)((a.M + kFixTokens - 1) / kFixTokens));
-    static bool fix_configured = false;
-    if (!fix_configured) {
-        if (cudaFuncSetAttribute(rows_fixup, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fixup_smem(256)) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        fix_configured = true;
-    }
-    (void)launch_dependent(rows_fixup, grid, dim3(kFixThreads), fixup_smem(a.r), stream, f);
-    QLORA_CHECK_LAUNCH();
+    // tokens of a fix-up CTA: 8 for the shortest chain of latencies, 16 when the tokens would otherwise
+    // take several waves of CTAs
+    QLORA_TRY(a.M <= 64 ? launch_fixup<4>(f, stream) : launch_fixup<8>(f, stream));
     return QLORA_OK;
 }
 
