@@ -884,23 +884,25 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
     char* ws = static_cast<char*>(workspace);
     float* partial = reinterpret_cast<float*>(ws + lw.part);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
+    void* U2 = ws + lw.u2;
+    const void* B8 = B_all;
+    if (r % 8) {
+        TimerScope t(QLORA_TIMER_LORA, s);
+        QLORA_TRY(launch_pad_rows(B_all, n_adapters * N, r, ws + lw.b8, s));
+        B8 = ws + lw.b8;
+    }
     if (M <= kRowsMaxM) {
         RowsArgs a{};
-        a.w = w; a.X = X; a.A = A_all; a.B = B_all; a.idx = adapter_idx; a.scales = scales; a.n_adapters = n_adapters;
-        a.r = r; a.M = M; a.out = Y; a.out_f32 = (y_dtype == QLORA_DTYPE_F32); a.U = U_save; a.workspace = ws + lw.part;
+        a.w = w; a.X = X; a.A = A_all; a.B = B8; a.ldb = round_up(r, 8); a.U2 = U2; a.R = half_width(r);
+        a.idx = adapter_idx; a.scales = scales; a.n_adapters = n_adapters; a.r = r; a.M = M;
+        a.out = Y; a.out_f32 = (y_dtype == QLORA_DTYPE_F32); a.U = U_save; a.workspace = ws + lw.part;
         TimerScope t(QLORA_TIMER_DECODE, s);
         return launch_rows(a, s);
     }
     const AdapterLists l = lists_at(ws, lw);
-    void* U2 = ws + lw.u2;
-    const void* B8 = B_all;
     {
         TimerScope t(QLORA_TIMER_LORA, s);
         QLORA_TRY(launch_lists(adapter_idx, M, n_adapters, lw, l, false, s));
-        if (r % 8) {
-            QLORA_TRY(launch_pad_rows(B_all, n_adapters * N, r, ws + lw.b8, s));
-            B8 = ws + lw.b8;
-        }
         int splits = 0;
         QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
         QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, U_save, U2, f16, s));

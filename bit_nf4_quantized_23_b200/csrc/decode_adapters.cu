@@ -12,8 +12,8 @@
 //
 // Work units are 256 rows x 64 of K; the units, tile major, are cut into equal contiguous ranges, one
 // per CTA (one CTA per SM), and every (tile, CTA) piece is a segment accumulated in TMEM and written as
-// an fp32 partial tile to slot tile + CTA.  rows_fixup sums each tile's slots in CTA order, adds the
-// adapter term s_a U B_a^T in fp32 and writes Y.
+// an fp32 partial tile to slot tile + CTA.  rows_finish_U sums the adapters' tiles to U, tc_rows_fixup
+// the others, adds the adapter term s_a U B_a^T on the tensor cores and writes Y.
 //
 // The expansion of the codes bounds the kernel (byte permutes, about three ALU operations a weight on a
 // pipe of 64 a clock), so the other roles are kept short: a producer thread expands two blocks of 64
@@ -415,202 +415,252 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     }
 }
 
-// Y[m, n] = the sum of the partial tiles of n / 256 in CTA order + sum_j (s_a U[m, j]) B_a[n, j] (fp32),
-// rounded to the output type.  CTA (tile, y): the tile's 256 columns and the y-th 8 or 16 tokens; a thread has
-// one column and half of the tokens.  The kernel is a chain of memory latencies, so each link has all its
-// loads in flight: the B rows of the CTA's tokens come by cp.async, 32 KiB at a time, while U is summed
-// from its own partial tiles and the base product from its slots.  Neighbouring tokens of one request
-// are a run and share B.
-constexpr int kFixThreads = 512;
-constexpr int kFixLoads = 16;                     // loads of partial sums that a thread has in flight together
-constexpr int kFixChunks = 8;                     // 16-byte chunks (8 ranks) of B per column and pass, over all runs
+// The CTAs whose ranges hold the units of a tile: unit u belongs to the largest b with b units / G <= u,
+// that is b units < (u + 1) G.
+__device__ __forceinline__ int2 tile_span(int tile, int steps, int64_t units, int G) {
+    const int64_t u = (int64_t)tile * steps;
+    return make_int2((int)(((u + 1) * G - 1) / units), (int)(((u + steps) * G - 1) / units));
+}
 
 struct FixParams {
     const float* partial;
     const int32_t* meta;
     const int32_t* idx;
     const float* scales;
-    const uint16_t* B;
     float* U;
+    uint16_t* U2;
     void* out;
     int64_t N;
-    int32_t M, r, rp, steps, w_tiles, G;
+    int32_t M, r, R, rp, steps, w_tiles, G;
     uint32_t nt;
     int32_t out_f32, f16;
+    uint32_t* err;
 };
 
-__host__ __device__ inline uint32_t fixup_smem(int r, int tokens) {
-    return kFixChunks * 256 * 16 + (uint32_t)tokens * (uint32_t)((r + 7) / 8 * 8) * 4;
+// U[m, j] = the sum of its partial tiles in CTA order (stored when the caller keeps U), and the hi/lo
+// halves of s_a U[m, j] in the 16-bit compute type, U2 [M, 2R]: zeros for j >= r and without an adapter.
+__global__ void __launch_bounds__(128)
+rows_finish_U(FixParams p) {
+    grid_dependency_wait();
+    allow_dependents();
+    const int i = (int)(blockIdx.x * 128 + threadIdx.x), m = i / p.R, j = i - m * p.R;
+    if (m >= p.M) return;
+    const int place = p.meta[1 + m], per_tile = adapters_per_tile(p.rp);
+    const int u_tiles = (p.meta[0] + per_tile - 1) / per_tile;
+    float v = 0.f, sv = 0.f;
+    if (place >= 0 && j < p.r) {
+        const float sc = __ldg(p.scales + p.idx[m]);
+        const int t = place / per_tile, row = (place - t * per_tile) * p.rp + j;
+        const int64_t slot_floats = (int64_t)p.nt * 256;
+        const int2 sp = tile_span(t, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
+        const float* src = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)m * 256 + row;
+        for (int b = sp.x; b <= sp.y; b += 8, src += 8 * slot_floats) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = b + e <= sp.y ? src[e * slot_floats] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v = __fadd_rn(v, x[e]);
+        }
+        sv = __fmul_rn(sc, v);
+    }
+    if (p.U && j < p.r) p.U[(int64_t)m * p.r + j] = v;
+    const bool f16 = p.f16 != 0;
+    const uint32_t hi = to16_rn(sv, f16);
+    p.U2[(int64_t)m * 2 * p.R + j] = (uint16_t)hi;
+    p.U2[(int64_t)m * 2 * p.R + p.R + j] = (uint16_t)to16_rn(__fsub_rn(sv, from16(hi, f16)), f16);
 }
 
-// kFixOwn: tokens of a thread; a CTA has twice as many.
-template <int kFixOwn>
-__global__ void __launch_bounds__(kFixThreads, 2)
-rows_fixup(FixParams p) {
-    constexpr int kFixTokens = 2 * kFixOwn, kFixSlots = kFixLoads / kFixOwn;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint4* bs = reinterpret_cast<uint4*>(smem);               // bs[(run * pass_chunks + c) * 256 + column]
-    float* us = reinterpret_cast<float*>(smem + kFixChunks * 256 * 16);   // us[q * pitch + j] = s_a U[m0 + q, j]
-    __shared__ int32_t tok_place[kFixTokens], tok_adapter[kFixTokens], tok_run[kFixTokens], run_adapter[kFixTokens];
-    __shared__ int32_t runs_of;
-    __shared__ int2 span[129];                                // first and last CTA of each tile of A_all rows; [128]: this tile's
-    const int tid = threadIdx.x, col = tid & 255, q0 = (tid >> 8) * kFixOwn;
-    const int m0 = (int)blockIdx.y * kFixTokens, nm = min(p.M - m0, kFixTokens);
-    grid_dependency_wait();                                   // partial tiles are complete
-    const int per_tile = adapters_per_tile(p.rp);
-    const int u_tiles = (p.meta[0] + per_tile - 1) / per_tile;
-    const int64_t units = (int64_t)(u_tiles + p.w_tiles) * p.steps;
-    const int64_t slot_floats = (int64_t)p.nt * 256;
-    const int tile = u_tiles + (int)blockIdx.x;
-    // the CTA whose range holds unit u: the largest b with b units / G <= u, that is b units < (u + 1) G
-    auto cta_of = [&](int64_t u) { return (int)(((u + 1) * p.G - 1) / units); };
-    auto span_of = [&](int t) {
-        return make_int2(cta_of((int64_t)t * p.steps), cta_of((int64_t)t * p.steps + p.steps - 1));
-    };
-    if (tid >= 256 && tid - 256 < u_tiles) span[tid - 256] = span_of(tid - 256);
-    if (tid == 128) span[128] = span_of(tile);
-    if (tid < 32) {                                           // tokens, and the runs of equal adapters among them
-        const int place = tid < nm ? p.meta[1 + m0 + tid] : -1;
-        const int a = place >= 0 ? p.idx[m0 + tid] : -1;
-        const int before = __shfl_up_sync(0xffffffffu, a, 1);
-        const uint32_t starts = __ballot_sync(0xffffffffu, a >= 0 && (tid == 0 || a != before));
-        const int run = __popc(starts & (0xffffffffu >> (31 - tid))) - 1;
-        if (tid < kFixTokens) {
-            tok_place[tid] = place;
-            tok_adapter[tid] = a;
-            tok_run[tid] = a >= 0 ? run : -1;
-            if (starts >> tid & 1u) run_adapter[run] = a;
+// Y[m, n] = the sum of the partial tiles of n / 256 in CTA order + s_a U[m] B_a[n]^T, rounded to the
+// output type.  CTA x: columns 64 x .. 64 x + 63 of every token (128 accumulator rows).  The adapter term
+// is the fused GEMM's: hi and lo of s_a U meet the adapter's B on the tensor cores, and the MMAs of one
+// adapter write only its tokens' rows.  The four epilogue warps sum the base product meanwhile.
+// Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 one thread per token.
+constexpr int kFixThreads = 192;
+constexpr uint32_t kFixB = 64 * 128;              // B stage: 64 columns of the output x 64 ranks
+constexpr int kFixStages = 4;
+constexpr uint32_t kFixU = 128 * 128;             // one 64-wide image of U2
+
+struct FixLayout {
+    uint32_t off_b, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
+};
+__host__ __device__ inline FixLayout fix_layout(uint32_t images) {
+    FixLayout l;
+    l.off_b = images * kFixU;
+    l.off_mask = l.off_b + kFixStages * kFixB;
+    l.off_adapter = l.off_mask + 128 * 16;
+    l.off_bars = l.off_adapter + 128 * 4;
+    l.off_slot = l.off_bars + (2 * kFixStages + 2) * 8;
+    l.off_abort = l.off_slot + 4;
+    l.alloc = l.off_abort + 4 + 1024;
+    return l;
+}
+
+__global__ void __launch_bounds__(kFixThreads)
+tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ CUtensorMap tmB, FixParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - ptx::smem_addr(smem_raw));
+    const int images = 2 * p.R / 64;
+    const FixLayout lay = fix_layout((uint32_t)images);
+    const uint32_t sU = base, sB = base + lay.off_b;
+    const uint32_t bar_full = base + lay.off_bars, bar_empty = bar_full + 8 * kFixStages;
+    const uint32_t bar_u = bar_empty + 8 * kFixStages, bar_acc = bar_u + 8;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(gbase + lay.off_mask);       // [adapter place][4]: lanes it leaves alone
+    int32_t* adapter = reinterpret_cast<int32_t*>(gbase + lay.off_adapter);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + lay.off_slot);
+    volatile int* abort = reinterpret_cast<volatile int*>(gbase + lay.off_abort);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+
+    for (int i = tid; i < 128 * 4; i += kFixThreads) mask[i] = 0xffffffffu;
+    if (tid == 0) {
+        for (int s = 0; s < kFixStages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        if (tid == 0) runs_of = __popc(starts);
+        ptx::mbar_init(bar_u, 1);
+        ptx::mbar_init(bar_acc, 1);
+        *abort = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+        ptx::tma_prefetch_map(&tmU2);
+        ptx::tma_prefetch_map(&tmB);
     }
+    if (warp == 1) {
+        ptx::tmem_alloc(base + lay.off_slot, 64);
+        ptx::tmem_relinquish();
+    }
+    grid_dependency_wait();                                   // partial tiles and U2 are complete
+    allow_dependents();
     __syncthreads();
-    const int runs = runs_of, all_chunks = (p.r + 7) / 8, pitch = all_chunks * 8;
-    // runs and chunks of B that are in shared memory together
-    const int pass_runs = min(runs, kFixChunks), pass_chunks = runs > 0 ? min(all_chunks, kFixChunks / pass_runs) : 0;
-    const int64_t n = (int64_t)blockIdx.x * 256 + col;
-    const bool in = n < p.N;
-    auto fetch = [&](int r0, int c0) {                        // B chunks c0 .. of runs r0 ..
-        const int nr = min(pass_runs, runs - r0), nc = min(pass_chunks, all_chunks - c0);
-        for (int e = tid >> 8; e < nr * nc && in; e += 2) {
-            const int run = e / nc, c = e - run * nc;
-            const uint16_t* src = p.B + ((int64_t)run_adapter[r0 + run] * p.N + n) * p.r + (c0 + c) * 8;
-            uint4* dst = bs + (run * pass_chunks + c) * 256 + col;
-            if ((p.r & 7) == 0) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(src) : "memory");
-            } else {                                          // rows of B start anywhere
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = (c0 + c) * 8 + i < p.r ? src[i] : 0u;
-                *dst = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-            }
-        }
-    };
-    fetch(0, 0);
-
-    // the base product: .x starts with it and takes the even ranks' terms, .y the odd ones'
-    float2 acc[kFixOwn];
-#pragma unroll
-    for (int q = 0; q < kFixOwn; ++q) acc[q] = make_float2(0.f, 0.f);
-    {
-        const int2 sp = span[128];
-        const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)(m0 + q0) * 256 + col;
-        for (int b = sp.x; b <= sp.y; b += kFixSlots, src += kFixSlots * slot_floats) {
-            float v[kFixSlots][kFixOwn];
-#pragma unroll
-            for (int e = 0; e < kFixSlots; ++e)
-#pragma unroll
-                for (int q = 0; q < kFixOwn; ++q)
-                    v[e][q] = q0 + q < nm && b + e <= sp.y ? src[e * slot_floats + q * 256] : 0.f;
-#pragma unroll
-            for (int e = 0; e < kFixSlots; ++e)
-#pragma unroll
-                for (int q = 0; q < kFixOwn; ++q) acc[q].x = __fadd_rn(acc[q].x, v[e][q]);
+    const int used = p.meta[0];
+    int place = -1;
+    if (warp >= 2) {                                          // one thread per token: the lanes of each adapter
+        const int m = tid - 64;
+        place = m < p.M ? p.meta[1 + m] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, place);
+        if (place >= 0 && lane == __ffs((int)same) - 1) {
+            mask[place * 4 + (m >> 5)] = ~same;
+            adapter[place] = p.idx[m];
         }
     }
-    for (int i = tid; i < kFixTokens * pitch; i += kFixThreads) {
-        const int q = i / pitch, j = i - q * pitch;
-        float v = 0.f, sc = 0.f;
-        if (j < p.r && tok_place[q] >= 0) {
-            sc = __ldg(p.scales + tok_adapter[q]);
-            const int t = tok_place[q] / per_tile, row = (tok_place[q] - t * per_tile) * p.rp + j;
-            const int2 sp = span[t];
-            const float* src = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)(m0 + q) * 256 + row;
-            for (int b = sp.x; b <= sp.y; b += 8, src += 8 * slot_floats) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = b + e <= sp.y ? src[e * slot_floats] : 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v = __fadd_rn(v, x[e]);
-            }
-        }
-        us[i] = __fmul_rn(sc, v);
-        if (p.U && blockIdx.x == 0 && q < nm && j < p.r) p.U[(int64_t)(m0 + q) * p.r + j] = v;
-    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int chunks = p.R >= 64 ? p.R / 64 : 1, steps = used * chunks;
 
-    const bool f16 = p.f16 != 0;
-    for (int r0 = 0; r0 < runs; r0 += pass_runs) {
-        for (int c0 = 0; c0 < all_chunks; c0 += pass_chunks) {
-            if (r0 > 0 || c0 > 0) {
-                __syncthreads();                              // the last pass has been read
-                fetch(r0, c0);
+    if (warp == 0) {
+        if (steps > 0 && ptx::elect_one_sync()) {
+            ptx::mbar_arrive_expect_tx(bar_u, (uint32_t)images * kFixU);
+            for (int c = 0; c < images; ++c) ptx::tma_load_2d(sU + c * kFixU, &tmU2, c * 64, 0, bar_u);
+        }
+        __syncwarp();
+        int issued = 0, s = 0;
+        uint32_t ph = 1;
+        for (int i = 0; i < steps; ++i) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * s, ph, abort, p.err))) break;
+            issued = i + 1;
+            const int d = i / chunks, c = i - d * chunks;
+            if (ptx::elect_one_sync()) {
+                ptx::mbar_arrive_expect_tx(bar_full + 8 * s, kFixB);
+                ptx::tma_load_2d(sB + s * kFixB, &tmB, c * 64, adapter[d] * (int32_t)p.N + (int32_t)blockIdx.x * 64,
+                                 bar_full + 8 * s);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncthreads();                                  // us and every thread's copies
-            const int nc = min(pass_chunks, all_chunks - c0);
-            for (int c = 0; c < nc; ++c) {
-                int have = -1;
-                float2 bv[4];
+            __syncwarp();
+            if (++s == kFixStages) { s = 0; ph ^= 1u; }
+        }
+        if (*abort) {   // drain this CTA's copies in flight before it exits
+            if (steps > 0) ptx::mbar_wait_drain(bar_u, 0);
+            for (int i = max(0, issued - kFixStages); i < issued; ++i)
+                ptx::mbar_wait_drain(bar_full + 8 * (i % kFixStages), (uint32_t)(i / kFixStages) & 1u);
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, 64, 0, 0), p.f16 != 0);
+        const uint64_t u_sw = ptx::smem_desc_sw128(sU, 16, 1024), b_sw = ptx::smem_desc_sw128(sB, 16, 1024);
+        const bool packed = p.R == 32;                        // hi and lo halves of 32 ranks in one image
+        bool ok = steps == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar_u, 0, abort, p.err));
+        int s = 0;
+        uint32_t ph = 0;
+        for (int i = 0; i < steps && ok; ++i) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_full + 8 * s, ph, abort, p.err));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const int d = i / chunks, c = i - d * chunks;
+            const uint4 mk = *reinterpret_cast<const uint4*>(mask + d * 4);
+            const uint32_t off[4] = {mk.x, mk.y, mk.z, mk.w};
+            if (ptx::elect_one_sync()) {
+                const uint64_t hi = u_sw + (uint32_t)c * (kFixU >> 4);
+                const uint64_t lo = packed ? hi + (64 >> 4) : hi + (uint32_t)chunks * (kFixU >> 4);
+                const uint64_t b = b_sw + (uint32_t)s * (kFixB >> 4);
+                for (int kk = 0; kk < (packed ? 2 : 4); ++kk) {
+                    ptx::mma_bf16_ss_lanes(tmem, hi + kk * 2, b + kk * 2, idesc, (c | kk) != 0 ? 1u : 0u, off);
+                    ptx::mma_bf16_ss_lanes(tmem, lo + kk * 2, b + kk * 2, idesc, 1u, off);
+                }
+                ptx::mma_commit(bar_empty + 8 * s);
+            }
+            __syncwarp();
+            if (++s == kFixStages) { s = 0; ph ^= 1u; }
+        }
+        if (ptx::elect_one_sync()) {
+            ptx::mma_commit(bar_acc);
+            if (*abort) ptx::mbar_wait_drain(bar_acc, 0);   // issued MMAs finish before TMEM is freed
+        }
+        __syncwarp();
+    } else {
+        const uint32_t quad = (uint32_t)(warp & 3);           // TMEM lanes that the warp reaches: its tokens
+        const int m = (int)(quad * 32u) + lane, col0 = (int)(blockIdx.x & 3u) * 64;
+        const int per_tile = adapters_per_tile(p.rp), u_tiles = (used + per_tile - 1) / per_tile;
+        const int tile = u_tiles + (int)(blockIdx.x >> 2);
+        const int2 sp = tile_span(tile, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
+        const bool has = m < p.M && p.meta[1 + m] >= 0;
+        const int64_t slot_floats = (int64_t)p.nt * 256;
+        const bool live = (int)(quad * 32u) < p.M;
+        float acc[64];
 #pragma unroll
-                for (int q = 0; q < kFixOwn; ++q) {
-                    const int run = tok_run[q0 + q] - r0;
-                    if (run < 0 || run >= pass_runs) continue;
-                    if (run != have) {
-                        have = run;
-                        const uint4 w = bs[(run * pass_chunks + c) * 256 + col];
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+        if (m < p.M) {
+            const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)m * 256 + col0;
+            for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
+                float4 v[16];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            bv[e] = make_float2(from16(x[e] & 0xFFFFu, f16), from16(x[e] >> 16, f16));
-                    }
-                    const float4* u4 = reinterpret_cast<const float4*>(us + (q0 + q) * pitch + (c0 + c) * 8);
-                    const float4 u0 = u4[0], u1 = u4[1];
-                    acc[q] = fma2_rn(make_float2(u0.x, u0.y), bv[0], acc[q]);
-                    acc[q] = fma2_rn(make_float2(u0.z, u0.w), bv[1], acc[q]);
-                    acc[q] = fma2_rn(make_float2(u1.x, u1.y), bv[2], acc[q]);
-                    acc[q] = fma2_rn(make_float2(u1.z, u1.w), bv[3], acc[q]);
+                for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const float4*>(src)[i];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[4 * i] = __fadd_rn(acc[4 * i], v[i].x);
+                    acc[4 * i + 1] = __fadd_rn(acc[4 * i + 1], v[i].y);
+                    acc[4 * i + 2] = __fadd_rn(acc[4 * i + 2], v[i].z);
+                    acc[4 * i + 3] = __fadd_rn(acc[4 * i + 3], v[i].w);
                 }
             }
         }
-    }
-    if (!in) return;
+        const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
+        ptx::tc_fence_after();
+        if (acc_ok && live) {
+            const int64_t n0 = (int64_t)blockIdx.x * 64;
 #pragma unroll
-    for (int q = 0; q < kFixOwn; ++q) {
-        if (q0 + q >= nm) break;
-        const int64_t at = (int64_t)(m0 + q0 + q) * p.N + n;
-        const float y = __fadd_rn(acc[q].x, acc[q].y);
-        if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)to16_rn(y, f16);
+            for (int c = 0; c < 2; ++c) {
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(tmem + ((quad * 32u) << 16) + c * 32, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = __float_as_uint(has ? __fadd_rn(acc[32 * c + i], __uint_as_float(v[i])) : acc[32 * c + i]);
+                if (m < p.M) store_row32(p.out, p.out_f32 != 0, p.f16 != 0, p.N, m, n0 + 32 * c, p.N, v);
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 64);
     }
 }
 
 // ---------------------------------------------------------------------------- host
 
 inline int32_t adapter_rows(int32_t r) { return (r + 7) / 8 * 8; }
-
-template <int OWN>
-qlora_status launch_fixup(const FixParams& f, cudaStream_t stream) {
-    static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
-    if (!configured) {
-        if (cudaFuncSetAttribute(rows_fixup<OWN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)fixup_smem(256, 2 * OWN)) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
-    const dim3 grid((unsigned)f.w_tiles, (unsigned)((f.M + 2 * OWN - 1) / (2 * OWN)));
-    (void)launch_dependent(rows_fixup<OWN>, grid, dim3(kFixThreads), fixup_smem(f.r, 2 * OWN), stream, f);
-    QLORA_CHECK_LAUNCH();
-    return QLORA_OK;
-}
 
 inline uint32_t token_tile(int64_t M) { return (uint32_t)((M + 7) / 8 * 8); }
 
@@ -664,13 +714,24 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     (void)launch_dependent(tc_rows_nf4, dim3((unsigned)G), dim3(kThreads), lay.alloc, stream, tmCodes, tmX, tmA, p);
     QLORA_CHECK_LAUNCH();
     FixParams f{};
-    f.partial = p.partial; f.meta = p.meta; f.idx = a.idx; f.scales = a.scales;
-    f.B = static_cast<const uint16_t*>(a.B); f.U = a.U; f.out = a.out; f.N = N;
-    f.M = p.M; f.r = p.r; f.rp = p.rp; f.steps = p.steps; f.w_tiles = p.w_tiles; f.G = (int32_t)G; f.nt = p.nt;
-    f.out_f32 = a.out_f32; f.f16 = p.f16;
-    // tokens of a fix-up CTA: 8 for the shortest chain of latencies, 16 when the tokens would otherwise
-    // take several waves of CTAs
-    QLORA_TRY(a.M <= 64 ? launch_fixup<4>(f, stream) : launch_fixup<8>(f, stream));
+    f.partial = p.partial; f.meta = p.meta; f.idx = a.idx; f.scales = a.scales; f.U = a.U; f.out = a.out; f.N = N;
+    f.U2 = static_cast<uint16_t*>(a.U2);
+    f.M = p.M; f.r = p.r; f.R = a.R; f.rp = p.rp; f.steps = p.steps; f.w_tiles = p.w_tiles; f.G = (int32_t)G;
+    f.nt = p.nt; f.out_f32 = a.out_f32; f.f16 = p.f16; f.err = p.err;
+    (void)launch_dependent(rows_finish_U, dim3((unsigned)((f.M * f.R + 127) / 128)), dim3(128), 0, stream, f);
+    QLORA_CHECK_LAUNCH();
+    static bool fix_configured = false;
+    if (!fix_configured) {
+        if (cudaFuncSetAttribute(tc_rows_fixup, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+            return QLORA_ERR_CUDA;
+        fix_configured = true;
+    }
+    CUtensorMap tmU2, tmB;
+    if (!make_tmap_2d(&tmU2, true, a.U2, 2 * a.R, a.M, 4 * a.R, 64, 128, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmB, true, a.B, a.ldb, (uint64_t)a.n_adapters * N, a.ldb * 2, 64, 64, true)) return QLORA_ERR_CUDA;
+    (void)launch_dependent(tc_rows_fixup, dim3((unsigned)((N + 63) / 64)), dim3(kFixThreads),
+                           fix_layout((uint32_t)(2 * a.R / 64)).alloc, stream, tmU2, tmB, f);
+    QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
 

@@ -85,41 +85,9 @@ __device__ __forceinline__ void raster_tile(int64_t t, int64_t mtiles, int64_t n
     nt = local / gm;
 }
 
-// Store 32 consecutive output columns nb .. nb+31 of row m (fp32, or rounded to the 16-bit
-// compute dtype); columns at or past nlim (the end of the tile or of the row) are skipped.
 __device__ __forceinline__ void store_row32(const TcGemmParams& p, int64_t m, int64_t nb, int64_t nlim,
                                             const uint32_t (&v)[32]) {
-    const bool full = (nb + 32 <= nlim);
-    if (p.out_f32) {
-        float* dst = static_cast<float*>(p.out) + m * p.ldo + nb;
-        if (full && (p.ldo & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                reinterpret_cast<uint4*>(dst)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (nb + i < nlim) dst[i] = __uint_as_float(v[i]);
-        }
-    } else {
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + m * p.ldo + nb;
-        const bool h = p.f16 != 0;
-        if (full && (p.ldo & 7) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 o;
-                o.x = pack16x2_rn(__uint_as_float(v[8 * i + 0]), __uint_as_float(v[8 * i + 1]), h);
-                o.y = pack16x2_rn(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]), h);
-                o.z = pack16x2_rn(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]), h);
-                o.w = pack16x2_rn(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]), h);
-                reinterpret_cast<uint4*>(dst)[i] = o;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (nb + i < nlim) dst[i] = (uint16_t)to16_rn(__uint_as_float(v[i]), h);
-        }
-    }
+    qlora::store_row32(p.out, p.out_f32 != 0, p.f16 != 0, p.ldo, m, nb, nlim, v);
 }
 
 // The row mask of a tile's adapter, inverted (a set bit keeps its accumulator row as it is): `words`

@@ -111,7 +111,10 @@ struct RowsArgs {
     const qlora_nf4_weight* w;
     const void* X;          // [M, K]
     const void* A;          // [n_adapters, r, K]
-    const void* B;          // [n_adapters, N, r]
+    const void* B;          // [n_adapters, N, ldb], rows of 16-byte multiples; columns r .. ldb - 1 are zeros
+    int64_t ldb;
+    void* U2;               // [M, 2R] 16-bit, written: hi and lo halves of s U
+    int32_t R;              // half width: 32, or a multiple of 64 of at least r
     const int32_t* idx;     // [M]
     const float* scales;    // [n_adapters]
     int32_t n_adapters, r;

@@ -1,5 +1,6 @@
-// Expansion of packed 4-bit codes to the 16-bit compute type, as the fused GEMMs' producer warps do
-// it: a 16-entry table per block of 64 weights held in registers, and byte permutes.
+// What the fused dequant-GEMMs share: the expansion of packed 4-bit codes to the 16-bit compute type by
+// their producer warps (a 16-entry table per block of 64 weights held in registers, and byte permutes)
+// and the output stores of their epilogues.
 #pragma once
 
 #include "qlora_internal.cuh"
@@ -99,6 +100,42 @@ template <uint32_t LBO>
 __device__ __forceinline__ void zero_row_kn(uint32_t row_addr) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) st_shared_v4(row_addr + c * LBO, make_uint4(0, 0, 0, 0));
+}
+
+// Store 32 consecutive output columns nb .. nb+31 of row m (fp32, or rounded to the 16-bit
+// compute dtype); columns at or past nlim (the end of the tile or of the row) are skipped.
+__device__ __forceinline__ void store_row32(void* out, bool out_f32, bool h, int64_t ldo, int64_t m, int64_t nb,
+                                            int64_t nlim, const uint32_t (&v)[32]) {
+    const bool full = (nb + 32 <= nlim);
+    if (out_f32) {
+        float* dst = static_cast<float*>(out) + m * ldo + nb;
+        if (full && (ldo & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(dst)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (nb + i < nlim) dst[i] = __uint_as_float(v[i]);
+        }
+    } else {
+        uint16_t* dst = static_cast<uint16_t*>(out) + m * ldo + nb;
+        if (full && (ldo & 7) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint4 o;
+                o.x = pack16x2_rn(__uint_as_float(v[8 * i + 0]), __uint_as_float(v[8 * i + 1]), h);
+                o.y = pack16x2_rn(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]), h);
+                o.z = pack16x2_rn(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]), h);
+                o.w = pack16x2_rn(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]), h);
+                reinterpret_cast<uint4*>(dst)[i] = o;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (nb + i < nlim) dst[i] = (uint16_t)to16_rn(__uint_as_float(v[i]), h);
+        }
+    }
 }
 
 }  // namespace qlora
