@@ -19,8 +19,10 @@
 // pipe of 64 a clock), so the other roles are kept short: a producer thread expands two blocks of 64
 // weights per handshake, the codes' stages are freed as soon as they are in registers, and a unit takes
 // four MMAs and two copies.
-// Roles (576 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-17 four groups of producer
-// warps that take units in turn; groups 0 and 1 also run the epilogues of even and odd segments.
+// Roles (608 threads): warp 0 TMA of the tokens (and A_all rows), warp 1 TMEM owner + MMA issuer, warp 2
+// TMA of the codes (a warp of its own: behind the token ring the codes came a unit too late, 77 against
+// {CODES} us at W[28672, 8192] and 112 tokens), warps 3-18 four groups of producer warps that take units in
+// turn; groups 0 and 1 also run the epilogues of even and odd segments.
 //
 // A parity wait tells apart only neighbouring phases, so no role may come to a barrier two phases
 // behind: each group has a row stage and a code stage of its own, an accumulator belongs to one group's
@@ -38,7 +40,7 @@ namespace qlora {
 namespace {
 
 constexpr int kGroups = 4;
-constexpr int kThreads = 64 + 128 * kGroups;
+constexpr int kThreads = 96 + 128 * kGroups;
 constexpr int kMaxCtas = 256;
 constexpr uint32_t kRowStage = 256 * 128;         // 256 rows x 64 16-bit elements
 constexpr uint32_t kCodeStage = 256 * 32;         // their packed codes, 32-byte swizzled
@@ -190,28 +192,17 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
 
     if (warp == 0) {
         // unit i: X into token slot i % XS once the MMA that read it before has completed, with it an
-        // A_all unit's rows into row stage i % 4; the codes of a W_hat unit into code stage i % 4 once its
-        // group has read the last ones
+        // A_all unit's rows into row stage i % 4
         bool ok = true;
         int issued = 0, tile = t0, step = step0, xs = 0, g = 0;
         uint32_t xph = 1, gph = 1;
         for (int i = 0; i < n && ok; ++i) {
             const bool is_w = i >= nu;
-            if (is_w) {
-                // stages that A_all units passed over have seen no phase: their first wait passes
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_cempty + 8 * g, (uint32_t)((i - nu) / kGroups + 1) & 1u,
-                                                             abort, p.err));
-                if (!ok) break;
-                if (ptx::elect_one_sync()) {
-                    ptx::mbar_arrive_expect_tx(bar_cfull + 8 * g, kCodeStage);
-                    ptx::tma_load_2d(sCodes + g * kCodeStage, &tmCodes, step * 32, (tile - u_tiles) * 256, bar_cfull + 8 * g);
-                }
-                __syncwarp();
-            }
             bool w = ptx::mbar_wait(bar_xempty + 8 * xs, xph, abort, p.err);
             if (w && !is_w) w = ptx::mbar_wait(bar_bempty + 8 * g, gph, abort, p.err);
             ok = __all_sync(0xffffffffu, w);
-            if (ok && ptx::elect_one_sync()) {
+            if (!ok) break;
+            if (ptx::elect_one_sync()) {
                 const uint32_t fb = bar_xfull + 8 * xs;
                 const int ad0 = tile * per_tile, ads = is_w ? 0 : min(per_tile, used - ad0);
                 ptx::mbar_arrive_expect_tx(fb, lay.x_stage + (uint32_t)(ads * p.rp) * 128u);
@@ -220,17 +211,36 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
                     ptx::tma_load_3d(sB + g * kRowStage + (uint32_t)(q * p.rp) * 128u, &tmA, step * 64, 0, list[ad0 + q], fb);
             }
             __syncwarp();
-            issued = ok ? i + 1 : i;
+            issued = i + 1;
             if (++step == S) { step = 0; ++tile; }
             if (++xs == XS) { xs = 0; xph ^= 1u; }
             if (++g == kGroups) { g = 0; gph ^= 1u; }
         }
-        if (*abort) {   // drain this CTA's copies in flight before it exits
+        if (*abort) {   // drain this warp's copies in flight before the CTA exits
             for (int c = max(0, issued - XS); c < issued; ++c)
                 ptx::mbar_wait_drain(bar_xfull + 8 * (c % XS), (uint32_t)(c / XS) & 1u);
-            // the codes of the unit after the last token tile may be in flight too
-            const int end = min(issued + 1, n);
-            for (int c = max(nu, end - kGroups); c < end; ++c)
+        }
+    } else if (warp == 2) {
+        // the codes of W_hat unit i into code stage i % 4 once its group has read the last ones.  Stages that
+        // A_all units passed over have seen no phase: their first wait passes.
+        bool ok = true;
+        int issued = nu;
+        int64_t u = u0 + nu;
+        int tile = (int)(u / S), step = (int)(u - (int64_t)tile * S), g = nu % kGroups;
+        for (int i = nu; i < n && ok; ++i) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_cempty + 8 * g, (uint32_t)((i - nu) / kGroups + 1) & 1u, abort, p.err));
+            if (!ok) break;
+            if (ptx::elect_one_sync()) {
+                ptx::mbar_arrive_expect_tx(bar_cfull + 8 * g, kCodeStage);
+                ptx::tma_load_2d(sCodes + g * kCodeStage, &tmCodes, step * 32, (tile - u_tiles) * 256, bar_cfull + 8 * g);
+            }
+            __syncwarp();
+            issued = i + 1;
+            if (++step == S) { step = 0; ++tile; }
+            if (++g == kGroups) g = 0;
+        }
+        if (*abort) {
+            for (int c = max(nu, issued - kGroups); c < issued; ++c)
                 ptx::mbar_wait_drain(bar_cfull + 8 * (c % kGroups), (uint32_t)((c - nu) / kGroups) & 1u);
         }
     } else if (warp == 1) {
@@ -281,7 +291,7 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
         __syncwarp();
     } else {
         // group g takes units g, g + 4, ...; thread t expands rows t and t + 128 of the unit's tile
-        const int g = (warp - 2) >> 2, t = tid - 64 - 128 * g;
+        const int g = (warp - 3) >> 2, t = tid - 96 - 128 * g;
         const float mu = p.c1f ? 0.f : *p.mu;
         // block constants of a unit, as loaded (any arithmetic here would wait for the loads): the E4M3
         // codes (or fp32 constants) of its two blocks and their c2.  `at` is the block index of row t.
@@ -592,7 +602,8 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
                 const uint64_t hi = u_sw + (uint32_t)c * (kFixU >> 4);
                 const uint64_t lo = packed ? hi + (64 >> 4) : hi + (uint32_t)chunks * (kFixU >> 4);
                 const uint64_t b = b_sw + (uint32_t)s * (kFixB >> 4);
-                for (int kk = 0; kk < (packed ? 2 : 4); ++kk) {
+                const int nk = min(4, (p.r - 64 * c + 15) / 16);   // 16-wide steps that hold ranks
+                for (int kk = 0; kk < nk; ++kk) {
                     ptx::mma_bf16_ss_lanes(tmem, hi + kk * 2, b + kk * 2, idesc, (c | kk) != 0 ? 1u : 0u, off);
                     ptx::mma_bf16_ss_lanes(tmem, lo + kk * 2, b + kk * 2, idesc, 1u, off);
                 }
