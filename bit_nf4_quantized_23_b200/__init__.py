@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 from ctypes import byref, c_float, c_size_t, c_uint32
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -347,34 +348,54 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
-def _need_here(name: str, *tensors):
-    """All tensors on the current CUDA device, where the library launches."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name}: every tensor must be on the current CUDA device cuda:{dev}, got {t.device}")
+def _need_on(t: torch.Tensor, dtype, name: str, shape, dev: int) -> int:
+    """_need, and on CUDA device `dev`, the current one, where the library launches; returns the address.
+    One pass over the attributes when all is well: these checks are a part of a small call's time."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name, shape)
+    raise ValueError(f"{name} must be on the current CUDA device cuda:{dev}, got {t.device}")
 
 
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The CUDA device of t, which has to be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+
+
+@lru_cache(maxsize=256)
 def qlora_adapters_workspace_size(M: int, N: int, K: int, r: int, n_adapters: int) -> int:
     n = c_size_t()
     check(lib().qlora_adapters_workspace_size(M, N, K, r, n_adapters, byref(n)), "qlora_adapters_workspace_size")
     return n.value
 
 
-def _adapter_args(where, w, X, A_all, B_all, adapter_idx, scales, workspace):
-    """Checks of both directions; returns (M, n_adapters, r, workspace)."""
-    if A_all.dim() != 3:
+def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev):
+    """Checks of both directions; returns (M, n_adapters, r, addresses in C order, workspace)."""
+    if not isinstance(A_all, torch.Tensor) or A_all.dim() != 3:
         raise ValueError("A_all must be 3-D [n_adapters, r, K]")
-    M, (n, r, _) = X.shape[0], A_all.shape
-    _need(X, w.compute_dtype, "X", (M, w.K))
-    _need(A_all, w.compute_dtype, "A_all", (n, r, w.K))
-    _need(B_all, w.compute_dtype, "B_all", (n, w.N, r))
-    _need(adapter_idx, torch.int32, "adapter_idx", (M,))
-    _need(scales, torch.float32, "scales", (n,))
+    M, (n, r, _), dt = X.shape[0], A_all.shape, w.compute_dtype
+    at = (_need_on(X, dt, "X", (M, w.K), dev), _need_on(A_all, dt, "A_all", (n, r, w.K), dev),
+          _need_on(B_all, dt, "B_all", (n, w.N, r), dev), _need_on(adapter_idx, torch.int32, "adapter_idx", (M,), dev),
+          _need_on(scales, torch.float32, "scales", (n,), dev))
+    if w.codes.get_device() != dev:
+        raise ValueError(f"the weight must be on the current CUDA device cuda:{dev}, got {w.codes.device}")
     if workspace is None:
         workspace = torch.empty(qlora_adapters_workspace_size(M, w.N, w.K, r, n), dtype=torch.uint8, device=X.device)
-    _need_here(where, w.codes, X, A_all, B_all, adapter_idx, scales, workspace)
-    return M, n, r, workspace
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on the current CUDA device cuda:{dev}")
+    return M, n, r, at, workspace
 
 
 def qlora_linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor, B_all: torch.Tensor,
@@ -384,23 +405,20 @@ def qlora_linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor
     """The adapters of many requests over one base, any number of tokens: Y[m] = X[m] W_hat^T +
     s_a (X[m] A_a^T) B_a^T with a = adapter_idx[m] (negative: base only) and s_a = scales[a].
     A_all [n, r, K] and B_all [n, N, r] in the compute dtype (smaller ranks zero-padded to r),
-    adapter_idx int32 [M], scales fp32 [n], all on the device.  Returns (Y, U) with U fp32 [M, r]
-    (or None)."""
-    M, n, r, workspace = _adapter_args("qlora_linear_fwd_adapters", w, X, A_all, B_all, adapter_idx, scales, workspace)
+    adapter_idx int32 [M], scales fp32 [n], all on the current device.  Returns (Y, U) with U fp32
+    [M, r] (or None)."""
+    dev = _device_of(X, "X")
+    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev)
     y_dtype = w.compute_dtype if y_dtype is None else y_dtype
     if out is None:
-        out = torch.empty(M, w.N, dtype=y_dtype, device=X.device)
-    _need(out, y_dtype, "Y", (M, w.N))
+        out = torch.empty((M, w.N), dtype=y_dtype, device=X.device)
+    y_at = _need_on(out, y_dtype, "Y", (M, w.N), dev)
     if save_U and U_out is None:
-        U_out = torch.empty(M, r, dtype=torch.float32, device=X.device)
-    if U_out is not None:
-        _need(U_out, torch.float32, "U", (M, r))
-    _need_here("qlora_linear_fwd_adapters", out, U_out)
-    ws = w.c_struct()
-    check(lib().qlora_linear_fwd_adapters(byref(ws), _ptr(X), M, _ptr(A_all), _ptr(B_all), n, _ptr(adapter_idx), r,
-                                          _ptr(scales), _ptr(out), _dtype_code(y_dtype), _ptr(U_out),
-                                          _ptr(workspace), workspace.numel(), _stream(stream)),
-          "qlora_linear_fwd_adapters")
+        U_out = torch.empty((M, r), dtype=torch.float32, device=X.device)
+    u_at = None if U_out is None else _need_on(U_out, torch.float32, "U", (M, r), dev)
+    check(lib().qlora_linear_fwd_adapters(byref(w.c_struct()), at[0], M, at[1], at[2], n, at[3], r, at[4], y_at,
+                                          _dtype_code(y_dtype), u_at, workspace.data_ptr(), workspace.numel(),
+                                          _stream_on(stream, dev)), "qlora_linear_fwd_adapters")
     return out, U_out
 
 
@@ -411,54 +429,51 @@ def qlora_linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A
                               dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """(dX, dA_all, dB_all) of <dY, Y> of qlora_linear_fwd_adapters: dA_all fp32 [n, r, K] and dB_all
     fp32 [n, N, r] hold every adapter's gradient over its own tokens.  dX is None when need_dX is False."""
-    M, n, r, workspace = _adapter_args("qlora_linear_bwd_adapters", w, X, A_all, B_all, adapter_idx, scales, workspace)
+    dev = _device_of(X, "X")
+    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev)
     dx_dtype = w.compute_dtype if dx_dtype is None else dx_dtype
-    _need(dY, w.compute_dtype, "dY", (M, w.N))
-    if U_saved is not None:
-        _need(U_saved, torch.float32, "U_saved", (M, r))
+    dy_at = _need_on(dY, w.compute_dtype, "dY", (M, w.N), dev)
+    u_at = None if U_saved is None else _need_on(U_saved, torch.float32, "U_saved", (M, r), dev)
     if need_dX and dX is None:
-        dX = torch.empty(M, w.K, dtype=dx_dtype, device=X.device)
-    if dX is not None:
-        _need(dX, dx_dtype, "dX", (M, w.K))
+        dX = torch.empty((M, w.K), dtype=dx_dtype, device=X.device)
+    dx_at = None if dX is None else _need_on(dX, dx_dtype, "dX", (M, w.K), dev)
     if dA is None:
-        dA = torch.empty(n, r, w.K, dtype=torch.float32, device=X.device)
+        dA = torch.empty((n, r, w.K), dtype=torch.float32, device=X.device)
     if dB is None:
-        dB = torch.empty(n, w.N, r, dtype=torch.float32, device=X.device)
-    _need(dA, torch.float32, "dA", (n, r, w.K))
-    _need(dB, torch.float32, "dB", (n, w.N, r))
-    _need_here("qlora_linear_bwd_adapters", dY, U_saved, dX, dA, dB)
-    ws = w.c_struct()
-    check(lib().qlora_linear_bwd_adapters(byref(ws), _ptr(X), _ptr(dY), M, _ptr(A_all), _ptr(B_all), n,
-                                          _ptr(adapter_idx), r, _ptr(scales), _ptr(U_saved), _ptr(dX),
-                                          _dtype_code(dx_dtype), _ptr(dA), _ptr(dB), _ptr(workspace),
-                                          workspace.numel(), _stream(stream)), "qlora_linear_bwd_adapters")
+        dB = torch.empty((n, w.N, r), dtype=torch.float32, device=X.device)
+    da_at = _need_on(dA, torch.float32, "dA", (n, r, w.K), dev)
+    db_at = _need_on(dB, torch.float32, "dB", (n, w.N, r), dev)
+    check(lib().qlora_linear_bwd_adapters(byref(w.c_struct()), at[0], dy_at, M, at[1], at[2], n, at[3], r, at[4], u_at,
+                                          dx_at, _dtype_code(dx_dtype), da_at, db_at, workspace.data_ptr(),
+                                          workspace.numel(), _stream_on(stream, dev)), "qlora_linear_bwd_adapters")
     return dX, dA, dB
 
 
-def _rows(t: torch.Tensor, name: str, shape=None):
-    """A 2-D CUDA tensor of a library dtype whose rows are contiguous; returns (dtype code, row stride)."""
+def _rows(t: torch.Tensor, name: str, dev: int, shape=None):
+    """A 2-D tensor of a library dtype on CUDA device `dev` whose rows are contiguous; returns (dtype
+    code, row stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _dtype_code(t.dtype)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}, "
                          f"got {tuple(t.shape)}")
-    M, V = t.shape
-    ld = t.stride(0) if M > 1 else max(V, 1)
-    if not t.is_cuda or (V > 1 and t.stride(1) != 1) or ld < V:
-        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+    (M, V), (ld, one) = t.shape, t.stride()
+    if M <= 1:
+        ld = max(V, 1)
+    if t.get_device() != dev or (V > 1 and one != 1) or ld < V:
+        raise ValueError(f"{name} must be a tensor on the current CUDA device with contiguous rows")
     return code, ld
 
 
-def _topk_args(logits, teacher_idx, teacher_logits):
-    z_code, ld = _rows(logits, "logits")
+def _topk_args(logits, teacher_idx, teacher_logits, dev):
+    z_code, ld = _rows(logits, "logits", dev)
     if not isinstance(teacher_idx, torch.Tensor) or teacher_idx.dim() != 2:
         raise ValueError("teacher_idx must be a 2-D tensor [M, k]")
-    k = teacher_idx.shape[1]
-    _need(teacher_idx, torch.int32, "teacher_idx", (logits.shape[0], k))
+    shape = (logits.shape[0], teacher_idx.shape[1])
     t_code = _dtype_code(teacher_logits.dtype)
-    _need(teacher_logits, teacher_logits.dtype, "teacher_logits", (logits.shape[0], k))
-    return z_code, ld, k, t_code
+    return (z_code, ld, shape[1], t_code, _need_on(teacher_idx, torch.int32, "teacher_idx", shape, dev),
+            _need_on(teacher_logits, teacher_logits.dtype, "teacher_logits", shape, dev))
 
 
 def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,
@@ -468,17 +483,16 @@ def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
     row's k teacher logits over T and q the student's over the whole vocabulary.  logits [M, V] (bf16,
     fp16 or fp32, rows contiguous), teacher_idx int32 [M, k] (-1: no entry), teacher_logits [M, k].
     Returns (loss, lse), fp32 [M]; the backward takes lse."""
-    z_code, ld, k, t_code = _topk_args(logits, teacher_idx, teacher_logits)
+    dev = _device_of(logits, "logits")
+    z_code, ld, k, t_code, i_at, t_at = _topk_args(logits, teacher_idx, teacher_logits, dev)
     M, V = logits.shape
     if loss is None:
         loss = torch.empty(M, dtype=torch.float32, device=logits.device)
     if lse is None:
         lse = torch.empty(M, dtype=torch.float32, device=logits.device)
-    _need(loss, torch.float32, "loss", (M,))
-    _need(lse, torch.float32, "lse", (M,))
-    _need_here("qlora_distill_topk_fwd", logits, teacher_idx, teacher_logits, loss, lse)
-    check(lib().qlora_distill_topk_fwd(_ptr(logits), z_code, ld, M, V, _ptr(teacher_idx), _ptr(teacher_logits),
-                                       t_code, k, float(temperature), _ptr(loss), _ptr(lse), _stream(stream)),
+    check(lib().qlora_distill_topk_fwd(logits.data_ptr(), z_code, ld, M, V, i_at, t_at, t_code, k, temperature,
+                                       _need_on(loss, torch.float32, "loss", (M,), dev),
+                                       _need_on(lse, torch.float32, "lse", (M,), dev), _stream_on(stream, dev)),
           "qlora_distill_topk_fwd")
     return loss, lse
 
@@ -488,19 +502,19 @@ def qlora_distill_topk_bwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
                            dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """d(sum_m dloss[m] loss[m]) / d logits, in d_dtype (the logits' dtype when None): the dY of the
     output projection's backward.  `dlogits` may be `logits` itself."""
-    z_code, ld, k, t_code = _topk_args(logits, teacher_idx, teacher_logits)
+    dev = _device_of(logits, "logits")
+    z_code, ld, k, t_code, i_at, t_at = _topk_args(logits, teacher_idx, teacher_logits, dev)
     M, V = logits.shape
-    _need(lse, torch.float32, "lse", (M,))
-    _need(dloss, torch.float32, "dloss", (M,))
+    lse_at = _need_on(lse, torch.float32, "lse", (M,), dev)
+    dloss_at = _need_on(dloss, torch.float32, "dloss", (M,), dev)
     if dlogits is None:
-        dlogits = torch.empty(M, V, dtype=logits.dtype if d_dtype is None else d_dtype, device=logits.device)
+        dlogits = torch.empty((M, V), dtype=logits.dtype if d_dtype is None else d_dtype, device=logits.device)
     elif d_dtype is not None and dlogits.dtype != d_dtype:
         raise TypeError(f"dlogits must be {d_dtype}, got {dlogits.dtype}")
-    d_code, ldd = _rows(dlogits, "dlogits", (M, V))
-    _need_here("qlora_distill_topk_bwd", logits, teacher_idx, teacher_logits, lse, dloss, dlogits)
-    check(lib().qlora_distill_topk_bwd(_ptr(logits), z_code, ld, M, V, _ptr(teacher_idx), _ptr(teacher_logits),
-                                       t_code, k, float(temperature), _ptr(lse), _ptr(dloss), _ptr(dlogits), d_code,
-                                       ldd, _stream(stream)), "qlora_distill_topk_bwd")
+    d_code, ldd = _rows(dlogits, "dlogits", dev, (M, V))
+    check(lib().qlora_distill_topk_bwd(logits.data_ptr(), z_code, ld, M, V, i_at, t_at, t_code, k, temperature,
+                                       lse_at, dloss_at, dlogits.data_ptr(), d_code, ldd, _stream_on(stream, dev)),
+          "qlora_distill_topk_bwd")
     return dlogits
 
 

@@ -367,44 +367,49 @@ tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CU
 
 // V[m, j] = the sum of the splits' partials, in split order (out, fp32 [M, r]; may be null), and the
 // hi/lo halves of s_a V[m, j] in the 16-bit compute type (V2 [M, 2R], zeros for j >= r and for tokens
-// without an adapter; may be null).  hi = t(v), lo = t(v - hi): together within 2^-17 of v in bf16.
-// With splits = 0 the values come from V itself (a saved U).
+// without an adapter).  hi = t(v), lo = t(v - hi): together within 2^-17 of v in bf16.  With splits = 0
+// the values are V itself (a saved U, [M, r]).  Blocks of y = 1 do the same for a second pair.
+struct FinishSource {
+    const float* from;
+    int splits;
+    float* out;
+    uint16_t* V2;
+};
 __global__ void __launch_bounds__(256)
-finish_part(const float* __restrict__ partial, int splits, int64_t M, int r, int Rn, int R,
-            const int32_t* __restrict__ tok, const float* __restrict__ scales, float* __restrict__ out,
-            uint16_t* __restrict__ V2, bool f16) {
+finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, const int32_t* __restrict__ tok,
+            const float* __restrict__ scales, bool f16) {
     grid_dependency_wait();
     allow_dependents();
+    const FinishSource& f = blockIdx.y == 0 ? s0 : s1;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= M * R) return;
     const int64_t m = i / R;
     const int j = (int)(i - m * R);
     const int32_t a = tok[m];
-    float v = 0.f;
+    float v = 0.f, sv = 0.f;
     if (j < r && a >= 0) {
-        if (splits == 0) {
-            v = partial[m * r + j];
+        const float scale = __ldg(scales + a);
+        if (f.splits == 0) {
+            v = f.from[m * r + j];
         } else {
             const int64_t stride = M * Rn;
-            const float* q = partial + m * Rn + j;
+            const float* q = f.from + m * Rn + j;
             int s = 0;
-            for (; s + 8 <= splits; s += 8) {
+            for (; s + 8 <= f.splits; s += 8) {
                 float w[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) w[u] = q[(s + u) * stride];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) v = __fadd_rn(v, w[u]);
             }
-            for (; s < splits; ++s) v = __fadd_rn(v, q[s * stride]);
+            for (; s < f.splits; ++s) v = __fadd_rn(v, q[s * stride]);
         }
+        sv = __fmul_rn(scale, v);
     }
-    if (out && j < r) out[m * r + j] = v;
-    if (V2) {
-        const float sv = (j < r && a >= 0) ? __fmul_rn(scales[a], v) : 0.f;
-        const uint32_t hi = to16_rn(sv, f16);
-        V2[m * 2 * R + j] = (uint16_t)hi;
-        V2[m * 2 * R + R + j] = (uint16_t)to16_rn(__fsub_rn(sv, from16(hi, f16)), f16);
-    }
+    if (f.out && j < r) f.out[m * r + j] = v;
+    const uint32_t hi = to16_rn(sv, f16);
+    f.V2[m * 2 * R + j] = (uint16_t)hi;
+    f.V2[m * 2 * R + R + j] = (uint16_t)to16_rn(__fsub_rn(sv, from16(hi, f16)), f16);
 }
 
 // ---------------------------------------------------------------------------- dA and dB
@@ -660,7 +665,16 @@ struct AdaptersWs {
     int64_t tiles512;
 };
 
-int part_splits(int64_t M, int64_t red, int32_t r) { return lora_splits(M, (int)((red + 63) / 64), (int)round_up(r, 64), false); }
+// Splits of the reduction of U or dU: two CTAs for each of 148 SMs (a count fixed here, so that the
+// workspace does not depend on the current device) while each has at least four steps of 64, rounded so
+// that no split is empty.
+int part_splits(int64_t M, int64_t red, int32_t r) {
+    const int64_t tiles = (M + kPartTile - 1) / kPartTile, steps = (red + 63) / 64;
+    const int64_t most = r <= 128 ? 2 * 148 : 148;            // CTAs that run together
+    const int64_t want = std::max<int64_t>(1, std::min(most / tiles, steps / 4));
+    const int64_t per = (steps + want - 1) / want;
+    return (int)((steps + per - 1) / per);
+}
 
 AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     AdaptersWs w;
@@ -772,14 +786,14 @@ qlora_status part_gemm(const void* S, int64_t M, int64_t red, int64_t ld, const 
     return launch_part<false>(tmS, tmV, p, splits, s);
 }
 
-qlora_status launch_finish(const float* partial, int splits, int64_t M, int32_t r, const AdapterLists& l,
-                           const float* scales, float* out, void* V2, bool f16, cudaStream_t s) {
+// One source, or two (s1.V2 set).
+qlora_status launch_finish(const FinishSource& s0, const FinishSource& s1, int64_t M, int32_t r, const AdapterLists& l,
+                           const float* scales, bool f16, cudaStream_t s) {
     const int32_t R = half_width(r);
     const int64_t blocks = (M * R + 255) / 256;
     if (blocks > INT32_MAX) return QLORA_ERR_SHAPE;
-    (void)launch_dependent(finish_part, dim3((unsigned)blocks), dim3(256), 0, s, partial, splits, M, (int)r,
-                           (int)round_up(r, 16), (int)R, (const int32_t*)l.tok, scales, out, static_cast<uint16_t*>(V2),
-                           f16);
+    (void)launch_dependent(finish_part, dim3((unsigned)blocks, s1.V2 ? 2u : 1u), dim3(256), 0, s, s0, s1, M, (int)r,
+                           (int)round_up(r, 16), (int)R, (const int32_t*)l.tok, scales, f16);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
@@ -905,7 +919,8 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
         QLORA_TRY(launch_lists(adapter_idx, M, n_adapters, lw, l, false, s));
         int splits = 0;
         QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
-        QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, U_save, U2, f16, s));
+        const FinishSource u{partial, splits, U_save, static_cast<uint16_t*>(U2)};
+        QLORA_TRY(launch_finish(u, FinishSource{}, M, r, l, scales, f16, s));
     }
     TimerScope t(QLORA_TIMER_FWD_MAIN, s);
     return adapters_gemm(w, X, K, M, U2, B8, (int32_t)round_up(r, 8), r, n_adapters, l, Y, y_dtype, false, s);
@@ -959,18 +974,21 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
         int splits = 0;
         if (!U_saved) {
             QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
-            QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, nullptr, U2, f16, s));
-        } else {
-            QLORA_TRY(launch_finish(U_saved, 0, M, r, l, scales, nullptr, U2, f16, s));
+            const FinishSource u{partial, splits, nullptr, static_cast<uint16_t*>(U2)};
+            QLORA_TRY(launch_finish(u, FinishSource{}, M, r, l, scales, f16, s));
         }
         QLORA_TRY(part_gemm(dY8, M, N, ldy, B8, true, round_up(r, 8), r, n_adapters, l, partial, f16, &splits, s));
-        QLORA_TRY(launch_finish(partial, splits, M, r, l, scales, nullptr, dU2, f16, s));
+        const FinishSource du{partial, splits, nullptr, static_cast<uint16_t*>(dU2)};
+        const FinishSource u{U_saved, 0, nullptr, U_saved ? static_cast<uint16_t*>(U2) : nullptr};
+        QLORA_TRY(launch_finish(du, u, M, r, l, scales, f16, s));
     }
-    // the adapter gradients run beside dX on the low-priority side stream and fill the SMs that its
-    // last wave of tiles leaves idle
-    cudaStream_t g = dX ? side_stream() : s;
+    // The adapter gradients run beside dX on the low-priority side stream and fill the SMs that its last
+    // wave of tiles leaves idle.  Below about ten microseconds of dX the fork and join take longer on the
+    // host than they save on the GPU, and the two run in turn.
+    const bool forked = dX && (double)M * (double)N * (double)K >= 5e9;
+    cudaStream_t g = forked ? side_stream() : s;
     cudaEvent_t join = nullptr;
-    if (dX) {
+    if (forked) {
         if (!g) return QLORA_ERR_CUDA;
         cudaEvent_t fork = nullptr;
         if (cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) != cudaSuccess) return QLORA_ERR_CUDA;
@@ -991,7 +1009,7 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
         TimerScope t(QLORA_TIMER_LORA, g);
         st = launch_grads(X, dY8, ldy, M, N, K, r, n_adapters, dU2, U2, l, f16, dA_all, dB_all, g);
     }
-    if (dX) {   // the caller's stream resumes after the adapter gradients too
+    if (forked) {   // the caller's stream resumes after the adapter gradients too
         const bool ok = cudaEventRecord(join, g) == cudaSuccess && cudaStreamWaitEvent(s, join, 0) == cudaSuccess;
         cudaEventDestroy(join);
         if (!ok && st == QLORA_OK) st = QLORA_ERR_CUDA;

@@ -68,8 +68,6 @@ def test_binding_refuses_wrong_tensors():
     X, A, B = (torch.zeros(s, dtype=BF16) for s in ((5, 128), (2, 8, 128), (2, 48, 8)))
     with pytest.raises(ValueError):                              # not on a CUDA device
         q4.qlora_linear_fwd_adapters(w, X, A, B, torch.zeros(5, dtype=torch.int32), torch.ones(2))
-    with pytest.raises(ValueError):
-        q4.qlora_linear_fwd_adapters(w, X, A[0], B, torch.zeros(5, dtype=torch.int32), torch.ones(2))
 
 
 # ---------------------------------------------------------------------------- GPU
@@ -168,6 +166,31 @@ SHAPES = [(1, 1, 64, 1, 1), (1, 64, 64, 8, 3), (16, 130, 128, 3, 4), (17, 130, 1
           (100, 1000, 1024, 8, 3), (128, 72, 256, 33, 5), (129, 72, 256, 32, 5), (256, 264, 192, 16, 30),
           (257, 264, 192, 64, 6), (300, 520, 1088, 96, 5), (513, 523, 640, 24, 7), (700, 96, 320, 200, 2),
           (1100, 280, 128, 256, 3), (1536, 512, 512, 12, 64)]
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors_on_the_gpu():
+    c = Case(20, 136, 128, 8, 3, "mixed")
+    for name, bad, error in (("X", c.X[:, :64], ValueError), ("X", c.X.half(), TypeError), ("A", c.A[0], ValueError),
+                             ("A", c.A[:, :4], ValueError), ("B", c.B[:2], ValueError), ("idx", c.idx.long(), TypeError),
+                             ("idx", c.idx[:5], ValueError), ("scales", c.scales.cpu(), ValueError),
+                             ("scales", c.scales.half(), TypeError), ("dY", c.dY.t(), ValueError)):
+        good = getattr(c, name)
+        setattr(c, name, bad)
+        with pytest.raises(error):
+            c.bwd()
+        if name != "dY":
+            with pytest.raises(error):
+                c.fwd()
+        setattr(c, name, good)
+    with pytest.raises(ValueError):
+        c.fwd(workspace=torch.empty(16, dtype=torch.uint8))
+    with pytest.raises(q4.QloraError):
+        c.fwd(workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError):
+        c.fwd(y_dtype=torch.float64)
+    with pytest.raises(q4.QloraError):
+        c.fwd(y_dtype=F16)                                       # not the weight's 16-bit type
 
 
 @pytest.mark.gpu

@@ -64,10 +64,26 @@ def test_binding_refuses_wrong_tensors():
     z, i, t = torch.zeros(2, 8), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3)
     with pytest.raises(ValueError):
         q4.qlora_distill_topk_fwd(z, i, t)                       # not on a CUDA device
-    with pytest.raises(ValueError):
-        q4.qlora_distill_topk_fwd(z[0], i, t)
     with pytest.raises(TypeError):
-        q4.qlora_distill_topk_fwd(z.double(), i, t)
+        q4.qlora_distill_topk_fwd([0.0], i, t)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors_on_the_gpu():
+    z, i, t = torch.zeros(2, 8).cuda(), torch.zeros(2, 3, dtype=torch.int32).cuda(), torch.zeros(2, 3).cuda()
+    v = torch.zeros(2).cuda()
+    for bad, error in (((z[0], i, t), ValueError), ((z.double(), i, t), TypeError), ((z.t(), i, t), ValueError),
+                       ((z, i.long(), t), TypeError), ((z, i[:1], t), ValueError), ((z, i, t[:, :2]), ValueError),
+                       ((z, i.cpu(), t), ValueError)):
+        with pytest.raises(error):
+            q4.qlora_distill_topk_fwd(*bad)
+    for bad in ((z, i, t, v[:1], v), (z, i, t, v, v[:1])):
+        with pytest.raises(ValueError):
+            q4.qlora_distill_topk_bwd(*bad)
+    with pytest.raises(ValueError):
+        q4.qlora_distill_topk_bwd(z, i, t, v, v, dlogits=z[:1])
+    with pytest.raises(TypeError):
+        q4.qlora_distill_topk_bwd(z, i, t, v, v, d_dtype=torch.bfloat16, dlogits=z)
 
 
 # ---------------------------------------------------------------------------- GPU
