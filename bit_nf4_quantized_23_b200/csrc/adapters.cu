@@ -29,7 +29,6 @@ namespace qlora {
 namespace {
 
 constexpr int kPartTile = 128;                    // token rows of a U / dU tile
-constexpr int kPartEntry = 8;                     // words: row mask [4], adapter, 3 unused
 constexpr int kGradTile = 64;                     // tokens of one reduction step of dA / dB
 constexpr uint32_t kStage16K = 128 * 128;
 constexpr uint32_t kMaxSmem = 227 * 1024;
@@ -41,56 +40,63 @@ struct AdapterLists {
     int32_t* tok;             // [M] adapter of each token, -1 for none or an index out of range
     uint32_t* n512;           // [tiles of 512] entries of the tile
     uint32_t* e512;           // [tiles of 512][cap512][kAdEntry]
-    uint32_t* n128;           // [tiles of 128]
-    uint32_t* e128;           // [tiles of 128][cap128][kPartEntry]
     uint32_t* n_grad;         // [n_adapters] token tiles of 64 that hold the adapter
     uint4* e_grad;            // [n_adapters][tiles of 64]: tile, row mask (2 words), 1 if no other rows
-    int32_t cap512, cap128;
+    int32_t cap512;
     int32_t tiles64;
 };
 
-// Block b < tiles512: the lists of tokens 512 b .. 512 b + 511, one thread per token.  The first token
-// of a tile with an adapter opens its entry (entries in order of first appearance, so the lists do not
-// depend on timing), and each warp's tokens of one adapter write one word of its mask.
+// Block b < tiles512: the list of tokens 512 b .. 512 b + 511, one thread per token.  The first token of
+// the tile with an adapter opens its entry (entries in order of first appearance, so the lists do not
+// depend on timing), and each warp's tokens of one adapter write one word of its mask.  The first token
+// comes from a minimum per adapter in shared memory (up to 8192 adapters; a search of the tile above).
 // Block tiles512 + a: the token tiles of adapter a.
+constexpr int kTableAdapters = 8192;
+constexpr int kGradBatch = 4;                     // 512-token pieces whose indices are loaded together
+
 __global__ void __launch_bounds__(512)
 build_lists(const int32_t* __restrict__ idx, int64_t M, int32_t n_adapters, int64_t tiles512, AdapterLists l,
             uint32_t* err) {
+    extern __shared__ int32_t table[];            // [n_adapters] first token of the tile, up to kTableAdapters
     grid_dependency_wait();
     allow_dependents();
     __shared__ __align__(16) int32_t ids[512];
     __shared__ int32_t slot[512];
-    __shared__ uint32_t ballots[16];
+    __shared__ uint32_t ballots[kGradBatch][16];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (blockIdx.x >= tiles512) {
         const int32_t a = (int32_t)(blockIdx.x - tiles512);
         uint4* out = l.e_grad + (int64_t)a * l.tiles64;
         int32_t found = 0;
-        for (int64_t m0 = 0; m0 < M; m0 += 512) {
-            const int64_t m = m0 + t;
-            const uint32_t mine = __ballot_sync(0xffffffffu, m < M && idx[m] == a);
-            if (lane == 0) ballots[warp] = mine;
-            __syncthreads();
-            int32_t before = 0, total = 0;
+        for (int64_t m0 = 0; m0 < M; m0 += 512 * kGradBatch) {
+            bool mine[kGradBatch];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const bool any = (ballots[2 * q] | ballots[2 * q + 1]) != 0;
-                before += any && q < t;
-                total += any;
+            for (int k = 0; k < kGradBatch; ++k) mine[k] = m0 + 512 * k + t < M && idx[m0 + 512 * k + t] == a;
+#pragma unroll
+            for (int k = 0; k < kGradBatch; ++k) {
+                const uint32_t b = __ballot_sync(0xffffffffu, mine[k]);
+                if (lane == 0) ballots[k][warp] = b;
             }
-            if (t < 8 && (ballots[2 * t] | ballots[2 * t + 1]) != 0) {
-                const int64_t left = M - (m0 + 64 * t);       // rows of this token tile
-                const uint32_t lo = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
-                const uint32_t hi = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1u : 0u;
-                const uint32_t b0 = ballots[2 * t], b1 = ballots[2 * t + 1];
-                out[found + before] = make_uint4((uint32_t)(m0 / 64 + t), b0, b1, (b0 == lo && b1 == hi) ? 1u : 0u);
+            __syncthreads();
+            if (warp == 0) {                                  // lane i: the token tile i of the batch
+                const uint32_t* w = &ballots[0][0] + 2 * lane;
+                const bool any = (w[0] | w[1]) != 0;
+                const uint32_t tiles = __ballot_sync(0xffffffffu, any);
+                if (any) {
+                    const int64_t left = M - (m0 + 64 * lane);    // rows of this token tile
+                    const uint32_t lo = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+                    const uint32_t hi = left >= 64 ? 0xffffffffu : left > 32 ? (1u << (left - 32)) - 1u : 0u;
+                    out[found + __popc(tiles & ((1u << lane) - 1u))] =
+                        make_uint4((uint32_t)(m0 / 64 + lane), w[0], w[1], (w[0] == lo && w[1] == hi) ? 1u : 0u);
+                }
+                found += __popc(tiles);
             }
-            found += total;
             __syncthreads();
         }
         if (t == 0) l.n_grad[a] = (uint32_t)found;
         return;
     }
+    const bool tabled = n_adapters <= kTableAdapters;
     const int64_t m = (int64_t)blockIdx.x * 512 + t;
     int32_t a = m < M ? idx[m] : -1;
     if (a >= n_adapters) {
@@ -99,28 +105,33 @@ build_lists(const int32_t* __restrict__ idx, int64_t M, int32_t n_adapters, int6
     }
     if (a < 0) a = -1;
     if (m < M) l.tok[m] = a;
-    ids[t] = a;
+    if (tabled)
+        for (int i = t; i < n_adapters; i += 512) table[i] = 512;
+    else
+        ids[t] = a;
     __syncthreads();
-    int f512 = t, f128 = t;                                   // first token of the tile with this adapter
-    const int sub = t & ~127;
-    for (int j = 508; j >= 0; j -= 4) {
-        const int4 v = *reinterpret_cast<const int4*>(ids + j);
-        const int j0 = v.x == a ? j : v.y == a ? j + 1 : v.z == a ? j + 2 : v.w == a ? j + 3 : 512;
-        if (j0 < f512) f512 = j0;
-        if (j0 >= sub && j0 < f128) f128 = j0;
-    }
     const uint32_t same = __match_any_sync(0xffffffffu, a);
-    const bool writes = a >= 0 && lane == __ffs((int)same) - 1;
-
-    // tiles of 512
-    bool first = a >= 0 && f512 == t;
-    uint32_t b = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) ballots[warp] = b;
+    const bool leads = a >= 0 && lane == __ffs((int)same) - 1;   // the warp's first token with the adapter
+    int f512 = t;
+    if (tabled) {
+        if (leads) atomicMin(table + a, t);
+        __syncthreads();
+        if (a >= 0) f512 = table[a];
+    } else {
+        for (int j = t & ~3; j >= 0; j -= 4) {
+            const int4 v = *reinterpret_cast<const int4*>(ids + j);
+            const int f = v.x == a ? j : v.y == a ? j + 1 : v.z == a ? j + 2 : v.w == a ? j + 3 : 512;
+            f512 = min(f512, f);
+        }
+    }
+    const bool first = a >= 0 && f512 == t;
+    const uint32_t b = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) ballots[0][warp] = b;
     __syncthreads();
     int before = __popc(b & ((1u << lane) - 1u)), total = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
-        const int c = __popc(ballots[w]);
+        const int c = __popc(ballots[0][w]);
         if (w < warp) before += c;
         total += c;
     }
@@ -134,35 +145,7 @@ build_lists(const int32_t* __restrict__ idx, int64_t M, int32_t n_adapters, int6
         e[4] = make_uint4((uint32_t)a, 0, 0, 0);
     }
     __syncthreads();
-    if (writes) e512[slot[f512] * kAdEntry + warp] = same;
-    __syncthreads();
-
-    // tiles of 128
-    first = a >= 0 && f128 == t;
-    b = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) ballots[warp] = b;
-    __syncthreads();
-    before = __popc(b & ((1u << lane) - 1u));
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const int c = __popc(ballots[(warp & ~3) + w]);
-        if (w < (warp & 3)) before += c;
-        total += c;
-    }
-    const int64_t tile128 = (int64_t)blockIdx.x * 4 + (t >> 7);
-    if (tile128 * 128 < M) {
-        uint32_t* e128 = l.e128 + tile128 * l.cap128 * kPartEntry;
-        if ((t & 127) == 0) l.n128[tile128] = (uint32_t)total;
-        if (first) {
-            slot[t] = before;
-            uint4* e = reinterpret_cast<uint4*>(e128 + (int64_t)before * kPartEntry);
-            e[0] = make_uint4(0, 0, 0, 0);
-            e[1] = make_uint4((uint32_t)a, 0, 0, 0);
-        }
-    }
-    __syncthreads();
-    if (writes && tile128 * 128 < M) l.e128[(tile128 * l.cap128 + slot[f128]) * kPartEntry + (warp & 3)] = same;
+    if (leads) e512[slot[f512] * kAdEntry + warp] = same;
 }
 
 // ---------------------------------------------------------------------------- U and dU
@@ -190,7 +173,7 @@ struct PartParams {
 };
 
 struct PartLayout {
-    uint32_t off_v, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
+    uint32_t off_v, off_mask, off_adapter, off_bars, off_slot, off_abort, off_count, alloc;
 };
 __host__ __device__ inline PartLayout part_layout(uint32_t s_stages, uint32_t v_stages, uint32_t v_tile) {
     PartLayout l;
@@ -200,7 +183,8 @@ __host__ __device__ inline PartLayout part_layout(uint32_t s_stages, uint32_t v_
     l.off_bars = l.off_adapter + 128 * 4;
     l.off_slot = l.off_bars + (2 * s_stages + 2 * v_stages + 1) * 8;
     l.off_abort = l.off_slot + 4;
-    l.alloc = l.off_abort + 4 + 1024;
+    l.off_count = l.off_abort + 4;
+    l.alloc = l.off_count + 4 + 1024;
     return l;
 }
 
@@ -227,14 +211,30 @@ tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CU
     const int64_t row0 = (int64_t)blockIdx.x * kPartTile;
     const int k_begin = blockIdx.y * p.ksteps_per_split;
     const int k_end = min(p.ksteps_total, k_begin + p.ksteps_per_split);
-    const int n_ad = (int)p.count[blockIdx.x];
-    const int nk = n_ad > 0 ? k_end - k_begin : 0;
-
-    if (threadIdx.x < n_ad) {
-        const uint32_t* e = p.entry + ((int64_t)blockIdx.x * p.cap + threadIdx.x) * kPartEntry;
-        const uint4 v = *reinterpret_cast<const uint4*>(e);
-        mask[threadIdx.x] = make_uint4(~v.x, ~v.y, ~v.z, ~v.w);
-        adapter[threadIdx.x] = (int32_t)e[4];
+    volatile int32_t* n_ads = reinterpret_cast<volatile int32_t*>(gbase + lay.off_count);
+    if (warp == 2) {                                          // the entries of the 512-token tile that reach this 128
+        const int64_t t512 = row0 / kAdTile;
+        const int listed = (int)p.count[t512];
+        const uint32_t* e = p.entry + t512 * p.cap * kAdEntry;
+        int found = 0;
+        for (int i0 = 0; i0 < listed; i0 += 32) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            int32_t a = 0;
+            if (i0 + lane < listed) {
+                const uint32_t* at = e + (int64_t)(i0 + lane) * kAdEntry;
+                v = *reinterpret_cast<const uint4*>(at + (row0 % kAdTile) / 32);
+                a = (int32_t)at[16];
+            }
+            const bool here = (v.x | v.y | v.z | v.w) != 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, here);
+            if (here) {
+                const int at = found + __popc(all & ((1u << lane) - 1u));
+                mask[at] = make_uint4(~v.x, ~v.y, ~v.z, ~v.w);
+                adapter[at] = a;
+            }
+            found += __popc(all);
+        }
+        if (lane == 0) *n_ads = found;
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < SS; ++s) {
@@ -260,6 +260,7 @@ tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CU
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const int n_ad = *n_ads, nk = n_ad > 0 ? k_end - k_begin : 0;
 
     if (warp == 0) {
         int s = 0, v = 0, s_issued = 0, v_issued = 0;
@@ -660,36 +661,33 @@ inline int32_t half_width(int32_t r) { return r <= 32 ? 32 : (int32_t)round_up(r
 //   and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
 //   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
 struct AdaptersWs {
-    size_t tok, n512, e512, n128, e128, n_grad, e_grad, u2, du2, part, b8, dy8, total;
-    int32_t cap512, cap128, tiles64;
+    size_t tok, n512, e512, n_grad, e_grad, u2, du2, part, b8, dy8, total;
+    int32_t cap512, tiles64;
     int64_t tiles512;
 };
 
 // Splits of the reduction of U or dU: two CTAs for each of 148 SMs (a count fixed here, so that the
-// workspace does not depend on the current device) while each has at least four steps of 64, rounded so
+// workspace does not depend on the current device) while each has at least two steps of 64, rounded so
 // that no split is empty.
 int part_splits(int64_t M, int64_t red, int32_t r) {
     const int64_t tiles = (M + kPartTile - 1) / kPartTile, steps = (red + 63) / 64;
     const int64_t most = r <= 128 ? 2 * 148 : 148;            // CTAs that run together
-    const int64_t want = std::max<int64_t>(1, std::min(most / tiles, steps / 4));
+    const int64_t want = std::max<int64_t>(1, std::min(most / tiles, steps / 2));
     const int64_t per = (steps + want - 1) / want;
     return (int)((steps + per - 1) / per);
 }
 
 AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     AdaptersWs w;
-    const int64_t R = half_width(r), Rn = round_up(r, 16), t128 = (M + 127) / 128;
+    const int64_t R = half_width(r), Rn = round_up(r, 16);
     w.tiles512 = (M + kAdTile - 1) / kAdTile;
     w.cap512 = (int32_t)std::min<int64_t>({(int64_t)kAdTile, n, M});
-    w.cap128 = (int32_t)std::min<int64_t>({(int64_t)kPartTile, n, M});
     w.tiles64 = (int32_t)((M + 63) / 64);
     size_t o = 0;
     auto piece = [&o](size_t bytes) { const size_t at = o; o += align_up(bytes, 256); return at; };
     w.tok = piece(M * 4);
     w.n512 = piece(w.tiles512 * 4);
     w.e512 = piece((size_t)w.tiles512 * w.cap512 * kAdEntry * 4);
-    w.n128 = piece(t128 * 4);
-    w.e128 = piece((size_t)t128 * w.cap128 * kPartEntry * 4);
     w.n_grad = piece(n * 4);
     w.e_grad = piece((size_t)n * w.tiles64 * 16);
     w.u2 = piece((size_t)M * 2 * R * 2);
@@ -708,11 +706,9 @@ AdapterLists lists_at(char* ws, const AdaptersWs& w) {
     l.tok = reinterpret_cast<int32_t*>(ws + w.tok);
     l.n512 = reinterpret_cast<uint32_t*>(ws + w.n512);
     l.e512 = reinterpret_cast<uint32_t*>(ws + w.e512);
-    l.n128 = reinterpret_cast<uint32_t*>(ws + w.n128);
-    l.e128 = reinterpret_cast<uint32_t*>(ws + w.e128);
     l.n_grad = reinterpret_cast<uint32_t*>(ws + w.n_grad);
     l.e_grad = reinterpret_cast<uint4*>(ws + w.e_grad);
-    l.cap512 = w.cap512; l.cap128 = w.cap128; l.tiles64 = w.tiles64;
+    l.cap512 = w.cap512; l.tiles64 = w.tiles64;
     return l;
 }
 
@@ -720,7 +716,8 @@ qlora_status launch_lists(const int32_t* idx, int64_t M, int32_t n, const Adapte
                           bool grads, cudaStream_t s) {
     uint32_t* err = device_error_word();
     if (!err) return QLORA_ERR_CUDA;
-    (void)launch_dependent(build_lists, dim3((unsigned)(w.tiles512 + (grads ? n : 0))), dim3(512), 0, s, idx, M, n,
+    const size_t table = n <= kTableAdapters ? (size_t)n * 4 : 0;
+    (void)launch_dependent(build_lists, dim3((unsigned)(w.tiles512 + (grads ? n : 0))), dim3(512), table, s, idx, M, n,
                            w.tiles512, l, err);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
@@ -744,9 +741,10 @@ qlora_status launch_part(const CUtensorMap& tmS, const CUtensorMap& tmV, PartPar
             return QLORA_ERR_CUDA;
         configured = true;
     }
-    // two CTAs per SM up to 128 ranks: 4 + 5 stages of 16 + 8 KiB, or 3 + 3 of 16 + 16 KiB
-    p.s_stages = p.v_tile <= 8192 ? 4 : 3;
-    p.v_stages = p.v_tile <= 8192 ? 5 : 3;
+    // two CTAs per SM up to 128 ranks: three S stages and the rest of 108 KiB for V tiles, of which a tile of
+    // many adapters takes many per S tile
+    p.s_stages = 3;
+    p.v_stages = std::min(16u, std::max(3u, (108u * 1024 - p.s_stages * kStage16K) / p.v_tile));
     const PartLayout lay = part_layout(p.s_stages, p.v_stages, p.v_tile);
     if (lay.alloc > kMaxSmem) return QLORA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)((p.M + kPartTile - 1) / kPartTile), (unsigned)splits);
@@ -771,7 +769,7 @@ qlora_status part_gemm(const void* S, int64_t M, int64_t red, int64_t ld, const 
     p.v_tile = v_mn ? (uint32_t)round_up(p.Rn, 64) * 128u : (uint32_t)p.Rn * 128u;
     p.v_tile = (uint32_t)round_up(p.v_tile, 1024);            // swizzle atoms stay aligned
     p.f16 = f16;
-    p.count = l.n128; p.entry = l.e128; p.cap = l.cap128; p.tok = l.tok;
+    p.count = l.n512; p.entry = l.e512; p.cap = l.cap512; p.tok = l.tok;
     p.partial = partial;
     p.err = device_error_word();
     if (!p.err) return QLORA_ERR_CUDA;

@@ -219,6 +219,13 @@ def test_few_tokens(M, N, K, r, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n,rows", [(600, 40, 64, 2, 9000, "mixed"), (4500, 72, 128, 8, 3, "runs"),
+                                            (2100, 136, 64, 16, 700, "mixed"), (4097, 64, 64, 8, 2, "mixed")])
+def test_many_adapters_and_many_tokens(M, N, K, r, n, rows):
+    check(Case(M, N, K, r, n, rows))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", ["one", "none"])
 @pytest.mark.parametrize("M,N,K,r,n", [(5, 130, 128, 8, 2), (90, 200, 256, 16, 3), (600, 264, 192, 40, 2)])
 def test_a_single_adapter_and_none_at_all(M, N, K, r, n, rows):
