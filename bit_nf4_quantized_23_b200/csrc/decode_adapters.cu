@@ -721,7 +721,12 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (!make_tmap_codes32(&tmCodes, w->codes, K / 2, N)) return QLORA_ERR_CUDA;
     if (!make_tmap_3d(&tmA, a.A, K, a.r, a.n_adapters, 64, (uint32_t)p.rp)) return QLORA_ERR_CUDA;
     if (!make_tmap_2d(&tmX, true, a.X, K, a.M, K * 2, 64, p.nt, true)) return QLORA_ERR_CUDA;
-    const int64_t G = std::min<int64_t>({(int64_t)p.w_tiles * p.steps, (int64_t)sms, (int64_t)kMaxCtas});
+    // At least sqrt(K / 64) / 2 units per CTA: a unit costs its CTA about what a further slot costs the
+    // fix-up, and a tile's slots are its K / 64 units over a CTA's number of them (W[1024, 1024]: 33 to
+    // 31 us at 100 tokens).
+    int64_t least = 1;
+    while (4 * least * least < p.steps) ++least;
+    const int64_t G = std::max<int64_t>(1, std::min<int64_t>({(int64_t)p.w_tiles * p.steps / least, (int64_t)sms, (int64_t)kMaxCtas}));
     (void)launch_dependent(tc_rows_nf4, dim3((unsigned)G), dim3(kThreads), lay.alloc, stream, tmCodes, tmX, tmA, p);
     QLORA_CHECK_LAUNCH();
     FixParams f{};

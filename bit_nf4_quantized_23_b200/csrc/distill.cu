@@ -153,83 +153,68 @@ struct DistillParams {
     uint32_t* err;
 };
 
-__device__ __forceinline__ float block_max(float v, float* red) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = red[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) r = fmaxf(r, red[w]);
-    __syncthreads();
-    return r;
-}
-
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) r += red[w];
-    __syncthreads();
-    return r;
-}
-
-// The teacher entries of thread tid in row m: e = tid + 256 q.  An index outside [0, V) is no
-// entry; one at or above V raises the BOUNDS flag too.
-struct Top {
-    int32_t i[kTopPerThread];
-    float t[kTopPerThread];    // teacher logit (-inf: no entry); then log2 p
+// A row's teacher entries in shared memory: index (-1: no entry) and teacher logit (-inf: no entry); the
+// student's logits there are in registers of the thread that loaded the entry, e = tid + 256 q, so that
+// nothing waits for them before their use.  An index outside [0, V) is no entry; one at or above V raises the BOUNDS flag.
+struct Entries {
+    int32_t i[kMaxTop];
+    float t[kMaxTop];
 };
-__device__ __forceinline__ void load_top(const DistillParams& p, int64_t m, Top& top) {
+
+// Fills the entries of row m; z only where the element lies in [lo, hi) or [0, head).  Returns whether
+// the calling thread met an entry that is not -inf.
+template <int DT_IN>
+__device__ __forceinline__ bool load_entries(const DistillParams& p, int64_t m, const void* row, int64_t lo, int64_t hi,
+                                             int64_t head, Entries& s, float (&z)[kTopPerThread]) {
+    bool any = false;
 #pragma unroll
     for (int q = 0; q < kTopPerThread; ++q) {
         const int e = threadIdx.x + q * kThreads;
-        top.i[q] = -1;
-        top.t[q] = -INFINITY;
-        if (e < p.k) {
-            const int32_t i = p.idx[m * p.k + e];
-            if (i >= 0 && i < p.V) {
-                top.i[q] = i;
-                top.t[q] = load_any(p.t, m * p.k + e, p.t_dtype);
-            } else if (i >= 0) {
-                atomicOr(p.err, ERR_FLAG_BOUNDS);
-            }
-        }
+        z[q] = 0.f;
+        if (e >= p.k) continue;
+        int32_t i = p.idx[m * p.k + e];
+        if (i >= p.V) atomicOr(p.err, ERR_FLAG_BOUNDS);
+        if (i < 0 || i >= p.V) i = -1;
+        const float t = i >= 0 ? load_any(p.t, m * p.k + e, p.t_dtype) : -INFINITY;
+        if (i >= 0 && ((i >= lo && i < hi) || i < head)) z[q] = load1<DT_IN>(row, i);
+        s.i[e] = i;
+        s.t[e] = t;
+        any |= !(t == -INFINITY);
     }
+    return any;
 }
 
-// Turns top.t into log2 p; returns whether the row has any entry.  The differences to the row's
-// largest logit are taken before the scaling, so rows of the type's lowest value stay finite.  The
-// maximum skips NaN and the sum does not: a NaN among the row's teacher logits gives NaN.
-__device__ __forceinline__ bool teacher_log2p(Top& top, float c, float* red) {
-    float mx = -INFINITY;
+// The teacher's softmax over the entries, by one warp: log2 p_e = (t_e - ref) c - l.  The differences to
+// the row's largest logit are taken before the scaling, so rows of the type's lowest value stay finite.
+// The maximum skips NaN and the sum does not: a NaN among the row's teacher logits gives NaN.
+struct Teacher {
+    float ref, l;
+    bool some;                 // the row has an entry
+};
+__device__ __forceinline__ Teacher teacher_softmax(const Entries& s, int k, float c) {
+    const int lane = threadIdx.x & 31;
+    float mx = -INFINITY, sum = 0.f;
+    for (int e = lane; e < k; e += 32) mx = fmaxf(mx, s.t[e]);
 #pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q) mx = fmaxf(mx, top.t[q]);
-    mx = block_max(mx, red);
-    const float r = Softmax2::ref(mx);
-    float s = 0.f;
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = Softmax2::ref(mx);
+    for (int e = lane; e < k; e += 32) sum += exp2f(__fmul_rn(__fsub_rn(s.t[e], ref), c));
 #pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q) {
-        top.t[q] = __fmul_rn(__fsub_rn(top.t[q], r), c);
-        s += exp2f(top.t[q]);
-    }
-    s = block_sum(s, red);
-    const float l = log2f(s);
-#pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q) top.t[q] = __fsub_rn(top.t[q], l);
-    return !(s == 0.f);
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return Teacher{ref, log2f(sum), !(sum == 0.f)};
+}
+__device__ __forceinline__ float log2_p(const Teacher& t, float logit, float c) {
+    return __fsub_rn(__fmul_rn(__fsub_rn(logit, t.ref), c), t.l);
 }
 
 // Row layout of a part: elements [0, head) one by one, then chunks of eight from `head` on, then
 // the tail one by one; head brings the chunks to 16-byte boundaries.
 template <int DT_IN>
-__global__ void __launch_bounds__(kThreads, 4) distill_fwd(DistillParams p) {
+__global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     grid_dependency_wait();
     allow_dependents();
-    __shared__ float red[kWarps];
+    __shared__ Entries entries;
+    __shared__ float entry_z[kMaxTop];
     __shared__ float2 joined[8];
     const int part = (int)(blockIdx.x % (unsigned)p.parts);
     const int64_t m = blockIdx.x / (unsigned)p.parts;
@@ -238,19 +223,14 @@ __global__ void __launch_bounds__(kThreads, 4) distill_fwd(DistillParams p) {
 
     // a cluster's CTAs have all started before one writes another's shared memory
     if (p.parts > 1) cg::this_cluster().barrier_arrive();
-    Top top;
-    float zt[kTopPerThread];                                  // student logits of the entries
-    if (part == 0) {
-        load_top(p, m, top);
-#pragma unroll
-        for (int q = 0; q < kTopPerThread; ++q) zt[q] = top.i[q] >= 0 ? load1<DT_IN>(row, top.i[q]) : 0.f;
-    }
+    float z[kTopPerThread];
+    if (part == 0) (void)load_entries<DT_IN>(p, m, row, 0, p.V, 0, entries, z);
 
     const int64_t head = min(p.V, (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kEs);
     const int64_t chunks = (p.V - head) / 8;
     const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
     Softmax2 acc{-INFINITY, 0.f};
-    constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 2 : 4; // 64 bytes of loads in flight per thread
+    constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : 6; // 96 bytes of loads in flight per thread: 174 us, 64 bytes 182
     int64_t c = c0 + threadIdx.x;
     for (; c + (kUnroll - 1) * kThreads < c1; c += kUnroll * kThreads) {
         Raw8<DT_IN> raw[kUnroll];
@@ -284,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, 4) distill_fwd(DistillParams p) {
         acc.join(m2, s2);
     }
     __shared__ float2 warp_acc[kWarps];
+    if (part == 0)
+#pragma unroll
+        for (int q = 0; q < kTopPerThread; ++q)
+            if ((int)threadIdx.x + q * kThreads < p.k) entry_z[threadIdx.x + q * kThreads] = z[q];
     if ((threadIdx.x & 31) == 0) warp_acc[threadIdx.x >> 5] = make_float2(acc.m, acc.s);
     __syncthreads();
     acc = Softmax2{warp_acc[0].x, warp_acc[0].y};
@@ -298,28 +282,28 @@ __global__ void __launch_bounds__(kThreads, 4) distill_fwd(DistillParams p) {
         acc = Softmax2{joined[0].x, joined[0].y};
         for (int w = 1; w < p.parts; ++w) acc.join(joined[w].x, joined[w].y);
     }
+    if (threadIdx.x >= 32) return;                            // one warp ends the row
     const float lse2 = acc.m + log2f(acc.s);
-    const bool some = teacher_log2p(top, p.c, red);
-    float part_loss = 0.f;
-#pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q) {
-        const float lp = top.t[q], pj = exp2f(lp);
-        if (top.i[q] >= 0 && !(pj == 0.f)) part_loss += pj * (lp - __fmaf_rn(zt[q], p.c, -lse2));
+    const Teacher teacher = teacher_softmax(entries, p.k, p.c);
+    float sum = 0.f;
+    for (int e = threadIdx.x; e < p.k; e += 32) {
+        const float lp = log2_p(teacher, entries.t[e], p.c), pe = exp2f(lp);
+        if (entries.i[e] >= 0 && !(pe == 0.f)) sum += pe * (lp - __fmaf_rn(entry_z[e], p.c, -lse2));
     }
-    const float sum = block_sum(part_loss, red);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (threadIdx.x == 0) {
         p.lse[m] = lse2 * kLn2;
-        p.loss[m] = some ? p.T2 * kLn2 * sum : 0.f;
+        p.loss[m] = teacher.some ? p.T2 * kLn2 * sum : 0.f;
     }
 }
 
 template <int DT_IN, int DT_OUT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) distill_bwd(DistillParams p) {
+__global__ void __launch_bounds__(kThreads, DT_IN != QLORA_DTYPE_F32 && DT_OUT != QLORA_DTYPE_F32 ? 5 : 4)
+distill_bwd(DistillParams p) {
     grid_dependency_wait();
     allow_dependents();
-    __shared__ float red[kWarps];
-    __shared__ int32_t s_i[kMaxTop];
-    __shared__ float s_p[kMaxTop];
+    __shared__ Entries entries;
     const int part = (int)(blockIdx.x % (unsigned)p.parts);
     // the rows run from the last to the first: what the forward has read last is still in L2
     const int64_t m = p.M - 1 - blockIdx.x / (unsigned)p.parts;
@@ -336,45 +320,17 @@ __global__ void __launch_bounds__(kThreads, 4) distill_bwd(DistillParams p) {
     const int64_t lo = VEC ? head + 8 * c0 : p.V * part / p.parts;
     const int64_t hi = VEC ? (last ? p.V : head + 8 * c1) : p.V * (part + 1) / p.parts;
 
-    const float g = p.dloss[m];
-    Top top;
-    load_top(p, m, top);
-    const bool zero = !teacher_log2p(top, p.c, red) || g == 0.f;
-    const float scale = g * p.T;
-    const float l2 = __fmul_rn(p.lse[m], (float)kLog2e);
-
-    if (!zero) {
-        // the entries' values: the first of equal indices carries the sum of their probabilities
-#pragma unroll
-        for (int q = 0; q < kTopPerThread; ++q) {
-            const int e = threadIdx.x + q * kThreads;
-            if (e < p.k) {
-                s_i[e] = top.i[q];
-                s_p[e] = exp2f(top.t[q]);
-            }
-        }
-    }
-    __syncthreads();
-    float fix[kTopPerThread];
-#pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q) {
-        const int e = threadIdx.x + q * kThreads;
-        if (e >= p.k || zero) top.i[q] = -1;
-        const int32_t i = top.i[q];
-        if (i < 0 || !((i >= lo && i < hi) || (last && i < head))) { top.i[q] = -1; continue; }
-        float sum = 0.f;
-        for (int o = 0; o < p.k; ++o) {
-            if (s_i[o] != i) continue;
-            if (o < e) { top.i[q] = -1; break; }
-            sum += s_p[o];
-        }
-        // read before the row is written: the gradient may take the logits' place
-        fix[q] = scale * (exp2_approx(__fmaf_rn(load1<DT_IN>(row, i), p.c, -l2)) - sum);
-    }
-    __syncthreads();
+    // Only what the dense pass must wait for comes before it: whether the row has an entry, and the
+    // entries' logits of this part, which it may overwrite (the gradient may take the logits' place).  The
+    // teacher's softmax follows the pass.
+    const float g = p.dloss[m], scale = g * p.T, l2 = __fmul_rn(p.lse[m], (float)kLog2e);
+    float z[kTopPerThread];
+    const bool entry = load_entries<DT_IN>(p, m, row, lo, hi, last ? head : 0, entries, z);
+    const bool zero = !__syncthreads_or(entry) || g == 0.f;
 
     if (VEC) {
-        constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 2 : 4;
+        // measured best of 2 to 8 loads per thread, and of 3 to 8 blocks per SM
+        constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : DT_OUT == QLORA_DTYPE_F32 ? 6 : 4;
         int64_t c = c0 + threadIdx.x;
         if (zero) {
             const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -414,10 +370,31 @@ __global__ void __launch_bounds__(kThreads, 4) distill_bwd(DistillParams p) {
         for (int64_t e = lo + threadIdx.x; e < hi; e += kThreads)
             store1<DT_OUT>(drow, e, zero ? 0.f : scale * exp2_approx(__fmaf_rn(load1<DT_IN>(row, e), p.c, -l2)));
     }
-    __syncthreads();
+    if (zero) return;
+
+    // the entries' elements: the first of equal indices carries the sum of their probabilities
+    const Teacher teacher = teacher_softmax(entries, p.k, p.c);   // every warp for itself
+    __syncthreads();                                          // every warp has read the entries
 #pragma unroll
-    for (int q = 0; q < kTopPerThread; ++q)
-        if (top.i[q] >= 0) store1<DT_OUT>(drow, top.i[q], fix[q]);
+    for (int q = 0; q < kTopPerThread; ++q) {
+        const int e = threadIdx.x + q * kThreads;
+        if (e < p.k) entries.t[e] = exp2f(log2_p(teacher, entries.t[e], p.c));
+    }
+    __syncthreads();                                          // the dense pass has been written, too
+#pragma unroll
+    for (int q = 0; q < kTopPerThread; ++q) {
+        const int e = threadIdx.x + q * kThreads;
+        const int32_t i = e < p.k ? entries.i[e] : -1;
+        if (i < 0 || !((i >= lo && i < hi) || (last && i < head))) continue;
+        float sum = 0.f;
+        bool first = true;
+        for (int o = 0; o < p.k; ++o) {
+            if (entries.i[o] != i) continue;
+            first &= o >= e;
+            sum += entries.t[o];
+        }
+        if (first) store1<DT_OUT>(drow, i, scale * (exp2_approx(__fmaf_rn(z[q], p.c, -l2)) - sum));
+    }
 }
 
 inline int elem_size(int dt) { return dt == QLORA_DTYPE_F32 ? 4 : 2; }

@@ -188,8 +188,10 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
                 } else {
                     const int j = MULTI ? je : it - ks0;
                     const int jb = p.b1_wrap ? j % p.b1_wrap : j;   // hi and lo steps share the B1 tile
-                    ptx::mbar_arrive_expect_tx(fa, L::kAStageBytes + kBStageBytes);
-                    ptx::tma_load_2d(a_dst, &tmA1, j * 64, (int32_t)m0, fa);
+                    // MULTI: the U2 tiles of the first adapter's steps serve the others'
+                    const bool load_a = !MULTI || p.ksteps1 > kStages || it < ks0 + p.ksteps1;
+                    ptx::mbar_arrive_expect_tx(fa, (load_a ? L::kAStageBytes : 0u) + kBStageBytes);
+                    if (load_a) ptx::tma_load_2d(a_dst, &tmA1, j * 64, (int32_t)m0, fa);
                     if (!DX) {
                         ptx::tma_load_2d(b_dst, &tmB1, jb * 64, (int32_t)n0 + (MULTI ? adapter * p.ad.rows : 0), fa);
                     } else {
@@ -239,7 +241,8 @@ tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CU
             if (!ok) break;
             ptx::tc_fence_after();
             if (ptx::elect_one_sync()) {
-                const uint64_t ad = adesc0 + ((uint32_t)s * (L::kAStageBytes >> 4));
+                const int sa = MULTI && p.ksteps1 <= kStages && it >= ks0 ? (ks0 + je) % kStages : s;
+                const uint64_t ad = adesc0 + ((uint32_t)sa * (L::kAStageBytes >> 4));
                 const bool kn = !DX && it < ks0;
                 const uint64_t bd = (kn ? bdesc0_kn : bdesc0) + ((uint32_t)s * (kBStageBytes >> 4));
                 const uint32_t kstep = DX ? (2048 >> 4) : kn ? ((2 * kBN * 16) >> 4) : (32 >> 4);
@@ -518,10 +521,12 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                 } else {
                     const int j = MULTI ? je : it - ks0;
                     const int jb = p.b1_wrap ? j % p.b1_wrap : j;   // hi and lo steps share the B1 tile
+                    // MULTI: the U2 tiles of the first adapter's steps serve the others'
+                    const bool load_a = !MULTI || p.ksteps1 > kPairStages || it < ks0 + p.ksteps1;
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s,
-                                                   2 * (kPairAStage + (DX ? kPairBStage : 128u * (uint32_t)hb)));
-                    ptx::tma_load_2d_pair(a_dst, &tmA1, j * 64, (int32_t)m0, lead_full_a + 8 * s);
+                        ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * ((load_a ? kPairAStage : 0u) +
+                                                                            (DX ? kPairBStage : 128u * (uint32_t)hb)));
+                    if (load_a) ptx::tma_load_2d_pair(a_dst, &tmA1, j * 64, (int32_t)m0, lead_full_a + 8 * s);
                     if (!DX) {
                         ptx::tma_load_2d_pair(sB + s * kPairBStage, &tmB1, jb * 64,
                                               (int32_t)nr0 + (MULTI ? adapter * p.ad.rows : 0), lead_full_a + 8 * s);
@@ -582,7 +587,8 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (ptx::elect_one_sync()) {
-                    const uint64_t ad = adesc0 + ((uint32_t)s * (kPairAStage >> 4));
+                    const int sa = MULTI && p.ksteps1 <= kPairStages && it >= ks0 ? (ks0 + je) & (kPairStages - 1) : s;
+                    const uint64_t ad = adesc0 + ((uint32_t)sa * (kPairAStage >> 4));
                     const bool kn = !DX && it < ks0;
                     const uint64_t bd = (kn ? bdesc0_kn : bdesc0) + ((uint32_t)s * (kPairBStage >> 4));
                     const uint32_t kstep = DX ? (2048 >> 4) : kn ? ((2 * 128 * 16) >> 4) : (32 >> 4);
@@ -1351,6 +1357,30 @@ static int pair_tile_width(int64_t M, int64_t N) {
     return best;
 }
 
+// The same choice for the forward with one adapter per token, whose batches are often below one wave: a
+// K-step of a pair tile takes about 66 + its width (in units of a column's share; measured at 400 tokens,
+// W[4096, 4096]: 49, 44, 39 and 34 us at 256, 224, 192 and 160 columns; odd multiples of 16 are slower).
+static int adapters_tile_width(int64_t M, int64_t N) {
+    const int64_t mtiles = (M + 511) / 512;
+    int best = kBN;
+    int64_t best_cost = INT64_MAX;
+    for (int bn : {256, 224, 192, 160}) {
+        const int64_t cost = (mtiles * ((N + bn - 1) / bn) + 73) / 74 * (66 + bn);
+        if (cost < best_cost) { best_cost = cost; best = bn; }
+    }
+    return best;
+}
+
+// One adapter per token: also up to 256 tokens on CTA pairs unless the single CTAs' tiles of 256
+// columns need so many fewer waves that they end first.  A K-step of a pair takes about two thirds of a
+// single CTA's (200 tokens, K = 8192: 96 against 127 us at N = 8192, one wave each; 185 against 132 us
+// at N = 28672, two waves of pairs).
+static bool use_pairs_adapters(int64_t M, int64_t Nout, int bn) {
+    if (M > 256) return true;
+    const int64_t pair_waves = ((Nout + bn - 1) / bn + 73) / 74, waves = ((Nout + kBN - 1) / kBN + 147) / 148;
+    return 2 * pair_waves <= 3 * waves;
+}
+
 // Splits of the reduction so that tiles x splits fills one wave of CTAs.
 static int64_t decode_grid(int64_t units, int sms) {
     return std::max<int64_t>(1, std::min<int64_t>({units, (int64_t)kDecCtasPerSm * sms, (int64_t)kDecMaxCtas}));
@@ -1419,11 +1449,12 @@ qlora_status launch_tc_decode(const DecodeArgs& a, cudaStream_t stream) {
 }
 
 qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
-    const uint32_t bm = a.p.M > 128 ? 256 : 128;
     const qlora_nf4_weight* w = a.w;
     const int64_t N = w->N, K = w->K;
-    const bool pair = use_pairs(a.p.M);
-    a.p.bn = (pair && !dx) ? pair_tile_width(a.p.M, N) : kBN;
+    const bool pair = a.n_adapters > 0 ? use_pairs_adapters(a.p.M, dx ? K : N, dx ? kBN : adapters_tile_width(a.p.M, N))
+                                       : use_pairs(a.p.M);
+    const uint32_t bm = pair || a.p.M > 128 ? 256 : 128;     // token rows of one copy: a pair CTA's, or the tile's
+    a.p.bn = !pair || dx ? kBN : a.n_adapters > 0 ? adapters_tile_width(a.p.M, N) : pair_tile_width(a.p.M, N);
     const uint32_t wrows = pair ? (uint32_t)a.p.bn / 2 : 256;   // forward: W rows one CTA loads codes (and LoRA B rows) for
     // segment 0: A (X or dY) and the packed codes
     if (!dx) {
