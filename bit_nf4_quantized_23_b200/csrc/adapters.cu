@@ -366,26 +366,36 @@ tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CU
     }
 }
 
-// V[m, j] = the sum of the splits' partials, in split order (out, fp32 [M, r]; may be null), and the
-// hi/lo halves of s_a V[m, j] in the 16-bit compute type (V2 [M, 2R], zeros for j >= r and for tokens
-// without an adapter).  hi = t(v), lo = t(v - hi): together within 2^-17 of v in bf16.  With splits = 0
-// the values are V itself (a saved U, [M, r]).  Blocks of y = 1 do the same for a second pair.
+// V[m, j] = the sum of the splits' partials, in split order (out, fp32 [M, r]; may be null), and s_a V[m, j]
+// as sums of 16-bit numbers of the compute type t, which the tensor cores need (zeros for j >= r and for
+// tokens without an adapter):
+//   V2 [M, 2R] (may be null): hi = t(v) and lo = t(v - hi), for the products that are rounded to 16 bits
+//   after them; together within 2^-17 of v in bf16.
+//   V3 [M, 3 Rg] (may be null): three parts, for the fp32 gradients; together within 2^-24 of v.  In fp16
+//   the second and third are kept 2^11 and 2^22 times too large, which their own accumulators undo:
+//   the residuals of a small gradient would otherwise fall below the type's range.  Ranks come in
+//   blocks of RB, each [part][RB].
+// With splits = 0 the values are V itself (a saved U, [M, r]).  Blocks of y = 1 do the same for a second
+// source.
 struct FinishSource {
     const float* from;
     int splits;
     float* out;
     uint16_t* V2;
+    uint16_t* V3;
 };
+constexpr float kPartScale = 2048.f;              // 2^11, fp16
+
 __global__ void __launch_bounds__(256)
-finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, const int32_t* __restrict__ tok,
-            const float* __restrict__ scales, bool f16) {
+finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, int RB, int Rg,
+            const int32_t* __restrict__ tok, const float* __restrict__ scales, bool f16) {
     grid_dependency_wait();
     allow_dependents();
     const FinishSource& f = blockIdx.y == 0 ? s0 : s1;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= M * R) return;
-    const int64_t m = i / R;
-    const int j = (int)(i - m * R);
+    if (i >= M * Rg) return;
+    const int64_t m = i / Rg;
+    const int j = (int)(i - m * Rg);
     const int32_t a = tok[m];
     float v = 0.f, sv = 0.f;
     if (j < r && a >= 0) {
@@ -409,24 +419,36 @@ finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, c
     }
     if (f.out && j < r) f.out[m * r + j] = v;
     const uint32_t hi = to16_rn(sv, f16);
-    f.V2[m * 2 * R + j] = (uint16_t)hi;
-    f.V2[m * 2 * R + R + j] = (uint16_t)to16_rn(__fsub_rn(sv, from16(hi, f16)), f16);
+    const float rest = __fsub_rn(sv, from16(hi, f16));
+    if (f.V2 && j < R) {
+        f.V2[m * 2 * R + j] = (uint16_t)hi;
+        f.V2[m * 2 * R + R + j] = (uint16_t)to16_rn(rest, f16);
+    }
+    if (f.V3) {
+        const float up = f16 ? kPartScale : 1.f;              // powers of two: exact
+        const uint32_t mid = to16_rn(__fmul_rn(rest, up), f16);
+        const float last = __fsub_rn(__fmul_rn(rest, up), from16(mid, f16));
+        uint16_t* at = f.V3 + m * 3 * Rg + (j / RB) * 3 * RB + j % RB;
+        at[0] = (uint16_t)hi;
+        at[RB] = (uint16_t)mid;
+        at[2 * RB] = (uint16_t)to16_rn(__fmul_rn(last, up), f16);
+    }
 }
 
 // ---------------------------------------------------------------------------- dA and dB
 
 // dA_a^T[k, j] = sum over the adapter's tokens of X[m, k] dU[m, j], and dB_a[n, j] likewise of dY and
-// s_a U, in one launch: CTA (x, a) computes 128 rows k (or n) of adapter a over the adapter's token
-// tiles.  Operand A is the [64 tokens x 128] tile of X or dY (MN-major), operand B the hi and lo halves
-// of dU or s U side by side (one MMA of N = 2R, the two halves added in fp32 in the epilogue) or, for
-// R > 128, one after the other into the same accumulator.
+// s_a U, in one launch: CTA (x, a, z) computes 128 rows k (or n) and rank block z of adapter a over the
+// adapter's token tiles.  Operand A is the [64 tokens x 128] tile of X or dY (MN-major), operand B the
+// three parts of dU or s U side by side, each with an accumulator of its own (one MMA of N = 3 RB, or one
+// of N = RB for each part when that exceeds 256); the epilogue adds the parts in fp32.
 // Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 zero the rows of other
 // tokens in tiles that the adapter shares, then run the epilogue.
 constexpr int kGradThreads = 192;
 
 struct GradParams {
     int64_t M, K, N;
-    int32_t r, R;
+    int32_t r, RB;            // ranks, and ranks of a block (z)
     int32_t tiles_k;          // CTAs x < tiles_k compute dA, the others dB
     uint32_t stages, v_bytes, tmem_cols;
     int32_t f16;
@@ -453,7 +475,7 @@ __host__ __device__ inline GradLayout grad_layout(uint32_t stages, uint32_t v_by
 
 __global__ void __launch_bounds__(kGradThreads, 2)
 tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmdY,
-                 const __grid_constant__ CUtensorMap tmdU2, const __grid_constant__ CUtensorMap tmU2, GradParams p) {
+                 const __grid_constant__ CUtensorMap tmdU3, const __grid_constant__ CUtensorMap tmU3, GradParams p) {
     grid_dependency_wait();
     allow_dependents();
     extern __shared__ uint8_t smem_raw[];
@@ -506,11 +528,12 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             if (ptx::elect_one_sync()) {
                 const uint32_t fb = bar_full + 8 * s, s_dst = sS + s * kStage16K, v_dst = sV + s * p.v_bytes;
                 const CUtensorMap* ms = is_a ? &tmX : &tmdY;
-                const CUtensorMap* mv = is_a ? &tmdU2 : &tmU2;
+                const CUtensorMap* mv = is_a ? &tmdU3 : &tmU3;
                 ptx::mbar_arrive_expect_tx(fb, kStage16K + p.v_bytes);
                 ptx::tma_load_2d(s_dst, ms, (int32_t)row0, tile * kGradTile, fb);
                 ptx::tma_load_2d(s_dst + 8192, ms, (int32_t)row0 + 64, tile * kGradTile, fb);
-                for (int c = 0; c < chunks; ++c) ptx::tma_load_2d(v_dst + c * 8192, mv, c * 64, tile * kGradTile, fb);
+                for (int c = 0; c < chunks; ++c)
+                    ptx::tma_load_2d(v_dst + c * 8192, mv, (int32_t)blockIdx.z * 3 * p.RB + c * 64, tile * kGradTile, fb);
             }
             __syncwarp();
             tile = next;
@@ -521,9 +544,9 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 ptx::mbar_wait_drain(bar_full + 8 * (i % S), (uint32_t)(i / S) & 1u);
         }
     } else if (warp == 1) {
-        const bool side = p.R <= 128;                         // hi and lo side by side in one MMA
+        const bool side = 3 * p.RB <= 256;                    // all parts in one MMA
         const uint32_t idesc =
-            ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, side ? 2 * p.R : p.R, 1, 1), p.f16 != 0);
+            ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, side ? 3 * p.RB : p.RB, 1, 1), p.f16 != 0);
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -536,11 +559,10 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint64_t ad_desc = ptx::smem_desc_sw128(a_base + kk * 2048, 8192, 1024);
-                    ptx::mma_bf16_ss(tmem, ad_desc, ptx::smem_desc_sw128(b_base + kk * 2048, 8192, 1024), idesc,
-                                     (i | kk) != 0 ? 1u : 0u);
-                    if (!side)
-                        ptx::mma_bf16_ss(tmem, ad_desc,
-                                         ptx::smem_desc_sw128(b_base + (p.R / 64) * 8192 + kk * 2048, 8192, 1024), idesc, 1u);
+                    for (int part = 0; part < (side ? 1 : 3); ++part)
+                        ptx::mma_bf16_ss(tmem + (uint32_t)(part * p.RB), ad_desc,
+                                         ptx::smem_desc_sw128(b_base + part * (p.RB / 64) * 8192 + kk * 2048, 8192, 1024),
+                                         idesc, (i | kk) != 0 ? 1u : 0u);
                 }
                 ptx::mma_commit(bar_empty + 8 * s);
             }
@@ -589,19 +611,23 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             const uint32_t quad = (uint32_t)(warp & 3);
             const int64_t orow = row0 + quad * 32 + lane;
             const bool in = orow < (is_a ? p.K : p.N);
-            float* dst = is_a ? p.dA + (int64_t)ad * p.r * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r;
+            const int j0 = (int)blockIdx.z * p.RB, nj = min(p.r - j0, p.RB);
+            float* dst = is_a ? p.dA + ((int64_t)ad * p.r + j0) * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r + j0;
             const bool vec = !is_a && p.r % 4 == 0;
+            const float down = p.f16 ? 1.f / kPartScale : 1.f;
 #pragma unroll 1
-            for (int c = 0; c * 16 < p.r; ++c) {
+            for (int c = 0; c * 16 < nj; ++c) {
                 float v[16];
                 if (nt > 0) {
-                    uint32_t hi[16], lo[16];
-                    ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + c * 16, hi);
-                    if (p.R <= 128) ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + p.R + c * 16, lo);
+                    uint32_t part[3][16];
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+                        ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + (uint32_t)(w * p.RB + c * 16), part[w]);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
-                        v[q] = p.R <= 128 ? __fadd_rn(__uint_as_float(hi[q]), __uint_as_float(lo[q])) : __uint_as_float(hi[q]);
+                        v[q] = __fmaf_rn(__fmaf_rn(__uint_as_float(part[2][q]), down, __uint_as_float(part[1][q])), down,
+                                         __uint_as_float(part[0][q]));
                 } else {                                      // no token has this adapter
 #pragma unroll
                     for (int q = 0; q < 16; ++q) v[q] = 0.f;
@@ -611,11 +637,11 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                 for (int q = 0; q < 16; q += 4) {
                     const int j = c * 16 + q;
                     if (vec) {
-                        if (j < p.r) *reinterpret_cast<float4*>(dst + j) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                        if (j < nj) *reinterpret_cast<float4*>(dst + j) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
                     } else {
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            if (j + u < p.r) dst[is_a ? (int64_t)(j + u) * p.K : j + u] = v[q + u];
+                            if (j + u < nj) dst[is_a ? (int64_t)(j + u) * p.K : j + u] = v[q + u];
                     }
                 }
             }
@@ -656,12 +682,16 @@ inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // Half width of the hi/lo operands: 32 (both halves share one 64-wide step) or a multiple of 64.
 inline int32_t half_width(int32_t r) { return r <= 32 ? 32 : (int32_t)round_up(r, 64); }
 
+// Ranks of a block of the gradients' three-part operands: 32, 64 or 128, and all blocks' ranks.
+inline int32_t grad_block(int32_t r) { return r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+inline int32_t grad_ranks(int32_t r) { return (int32_t)round_up(r, grad_block(r)); }
+
 // Workspace, every piece 256-byte aligned:
-//   the lists; U2 and dU2, 16-bit [M, 2R] (hi | lo of s U
-//   and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
+//   the lists; V2, 16-bit [M, 2R] (hi | lo of s U in the forward, of dU in the backward); U3 and dU3,
+//   16-bit [M, 3 Rg] (three parts of s U and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
 //   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
 struct AdaptersWs {
-    size_t tok, n512, e512, n_grad, e_grad, u2, du2, part, b8, dy8, total;
+    size_t tok, n512, e512, n_grad, e_grad, v2, u3, du3, part, b8, dy8, total;
     int32_t cap512, tiles64;
     int64_t tiles512;
 };
@@ -690,8 +720,9 @@ AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     w.e512 = piece((size_t)w.tiles512 * w.cap512 * kAdEntry * 4);
     w.n_grad = piece(n * 4);
     w.e_grad = piece((size_t)n * w.tiles64 * 16);
-    w.u2 = piece((size_t)M * 2 * R * 2);
-    w.du2 = piece((size_t)M * 2 * R * 2);
+    w.v2 = piece((size_t)M * 2 * R * 2);
+    w.u3 = piece((size_t)M * 3 * grad_ranks(r) * 2);
+    w.du3 = piece((size_t)M * 3 * grad_ranks(r) * 2);
     size_t part = (size_t)std::max(part_splits(M, K, r), part_splits(M, N, r)) * M * Rn * 4;
     if (M <= kRowsMaxM) part = std::max(part, rows_workspace_bytes(M, N, K, r, n));
     w.part = piece(part);
@@ -784,20 +815,20 @@ qlora_status part_gemm(const void* S, int64_t M, int64_t red, int64_t ld, const 
     return launch_part<false>(tmS, tmV, p, splits, s);
 }
 
-// One source, or two (s1.V2 set).
+// One source, or two (s1.V3 set).
 qlora_status launch_finish(const FinishSource& s0, const FinishSource& s1, int64_t M, int32_t r, const AdapterLists& l,
                            const float* scales, bool f16, cudaStream_t s) {
-    const int32_t R = half_width(r);
-    const int64_t blocks = (M * R + 255) / 256;
+    const int64_t blocks = (M * grad_ranks(r) + 255) / 256;
     if (blocks > INT32_MAX) return QLORA_ERR_SHAPE;
-    (void)launch_dependent(finish_part, dim3((unsigned)blocks, s1.V2 ? 2u : 1u), dim3(256), 0, s, s0, s1, M, (int)r,
-                           (int)round_up(r, 16), (int)R, (const int32_t*)l.tok, scales, f16);
+    (void)launch_dependent(finish_part, dim3((unsigned)blocks, s1.V3 ? 2u : 1u), dim3(256), 0, s, s0, s1, M, (int)r,
+                           (int)round_up(r, 16), (int)half_width(r), (int)grad_block(r), (int)grad_ranks(r),
+                           (const int32_t*)l.tok, scales, f16);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
 
 qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M, int64_t N, int64_t K, int32_t r,
-                          int32_t n, const void* dU2, const void* U2, const AdapterLists& l, bool f16, float* dA,
+                          int32_t n, const void* dU3, const void* U3, const AdapterLists& l, bool f16, float* dA,
                           float* dB, cudaStream_t s) {
     static bool configured = false;
     if (!configured) {
@@ -807,13 +838,13 @@ qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M,
         configured = true;
     }
     GradParams p{};
-    const int64_t R = half_width(r);
-    p.M = M; p.K = K; p.N = N; p.r = r; p.R = (int32_t)R;
+    const int32_t RB = grad_block(r), Rg = grad_ranks(r);
+    p.M = M; p.K = K; p.N = N; p.r = r; p.RB = RB;
     p.tiles_k = (int32_t)((K + 127) / 128);
     const int64_t tiles = p.tiles_k + (N + 127) / 128;
     if (tiles > INT32_MAX || n > 65535) return QLORA_ERR_SHAPE;
-    p.v_bytes = (uint32_t)(2 * R / 64) * 8192u;
-    p.tmem_cols = R <= 32 ? 64u : R <= 64 ? 128u : 256u;
+    p.v_bytes = (uint32_t)((3 * RB + 63) / 64) * 8192u;
+    p.tmem_cols = RB <= 32 ? 128u : RB <= 64 ? 256u : 512u;
     // as many stages as fit in half of the shared memory (two CTAs per SM), else one CTA's worth
     uint32_t stages = (kMaxSmem / 2 - 3072) / (kStage16K + p.v_bytes);
     if (stages < 2) stages = (kMaxSmem - 3072) / (kStage16K + p.v_bytes);
@@ -823,14 +854,14 @@ qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M,
     p.dA = dA; p.dB = dB;
     p.err = device_error_word();
     if (!p.err) return QLORA_ERR_CUDA;
-    CUtensorMap tmX, tmdY, tmdU2, tmU2;
+    CUtensorMap tmX, tmdY, tmdU3, tmU3;
     if (!make_tmap_2d(&tmX, true, X, K, M, K * 2, 64, 64, true)) return QLORA_ERR_CUDA;
     if (!make_tmap_2d(&tmdY, true, dY, N, M, ldy * 2, 64, 64, true)) return QLORA_ERR_CUDA;
-    if (!make_tmap_2d(&tmdU2, true, dU2, 2 * R, M, 4 * R, 64, 64, true)) return QLORA_ERR_CUDA;
-    if (!make_tmap_2d(&tmU2, true, U2, 2 * R, M, 4 * R, 64, 64, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmdU3, true, dU3, 3 * Rg, M, 6 * Rg, 64, 64, true)) return QLORA_ERR_CUDA;
+    if (!make_tmap_2d(&tmU3, true, U3, 3 * Rg, M, 6 * Rg, 64, 64, true)) return QLORA_ERR_CUDA;
     const GradLayout lay = grad_layout(p.stages, p.v_bytes);
-    (void)launch_dependent(tc_adapter_grads, dim3((unsigned)tiles, (unsigned)n), dim3(kGradThreads), lay.alloc, s, tmX,
-                           tmdY, tmdU2, tmU2, p);
+    (void)launch_dependent(tc_adapter_grads, dim3((unsigned)tiles, (unsigned)n, (unsigned)(Rg / RB)), dim3(kGradThreads),
+                           lay.alloc, s, tmX, tmdY, tmdU3, tmU3, p);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
@@ -896,7 +927,7 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
     char* ws = static_cast<char*>(workspace);
     float* partial = reinterpret_cast<float*>(ws + lw.part);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
-    void* U2 = ws + lw.u2;
+    void* U2 = ws + lw.v2;
     const void* B8 = B_all;
     if (r % 8) {
         TimerScope t(QLORA_TIMER_LORA, s);
@@ -917,7 +948,7 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
         QLORA_TRY(launch_lists(adapter_idx, M, n_adapters, lw, l, false, s));
         int splits = 0;
         QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
-        const FinishSource u{partial, splits, U_save, static_cast<uint16_t*>(U2)};
+        const FinishSource u{partial, splits, U_save, static_cast<uint16_t*>(U2), nullptr};
         QLORA_TRY(launch_finish(u, FinishSource{}, M, r, l, scales, f16, s));
     }
     TimerScope t(QLORA_TIMER_FWD_MAIN, s);
@@ -953,8 +984,9 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
     float* partial = reinterpret_cast<float*>(ws + lw.part);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
     const AdapterLists l = lists_at(ws, lw);
-    void* U2 = ws + lw.u2;
-    void* dU2 = ws + lw.du2;
+    uint16_t* dU2 = reinterpret_cast<uint16_t*>(ws + lw.v2);
+    uint16_t* U3 = reinterpret_cast<uint16_t*>(ws + lw.u3);
+    uint16_t* dU3 = reinterpret_cast<uint16_t*>(ws + lw.du3);
     const void* B8 = B_all;
     const void* dY8 = dY;
     const int64_t ldy = round_up(N, 8);
@@ -972,12 +1004,12 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
         int splits = 0;
         if (!U_saved) {
             QLORA_TRY(part_gemm(X, M, K, K, A_all, false, K, r, n_adapters, l, partial, f16, &splits, s));
-            const FinishSource u{partial, splits, nullptr, static_cast<uint16_t*>(U2)};
+            const FinishSource u{partial, splits, nullptr, nullptr, U3};
             QLORA_TRY(launch_finish(u, FinishSource{}, M, r, l, scales, f16, s));
         }
         QLORA_TRY(part_gemm(dY8, M, N, ldy, B8, true, round_up(r, 8), r, n_adapters, l, partial, f16, &splits, s));
-        const FinishSource du{partial, splits, nullptr, static_cast<uint16_t*>(dU2)};
-        const FinishSource u{U_saved, 0, nullptr, U_saved ? static_cast<uint16_t*>(U2) : nullptr};
+        const FinishSource du{partial, splits, nullptr, dX ? dU2 : nullptr, dU3};
+        const FinishSource u{U_saved, 0, nullptr, nullptr, U_saved ? U3 : nullptr};
         QLORA_TRY(launch_finish(du, u, M, r, l, scales, f16, s));
     }
     // The adapter gradients run beside dX on the low-priority side stream and fill the SMs that its last
@@ -1005,7 +1037,7 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
     }
     if (st == QLORA_OK) {
         TimerScope t(QLORA_TIMER_LORA, g);
-        st = launch_grads(X, dY8, ldy, M, N, K, r, n_adapters, dU2, U2, l, f16, dA_all, dB_all, g);
+        st = launch_grads(X, dY8, ldy, M, N, K, r, n_adapters, dU3, U3, l, f16, dA_all, dB_all, g);
     }
     if (forked) {   // the caller's stream resumes after the adapter gradients too
         const bool ok = cudaEventRecord(join, g) == cudaSuccess && cudaStreamWaitEvent(s, join, 0) == cudaSuccess;

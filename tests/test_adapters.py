@@ -107,6 +107,7 @@ class Case:
         s, idx, W, r = self.scales.double().cpu(), self.idx.cpu(), self.Wd, self.r
         M, K, N = X.shape[0], X.shape[1], dY.shape[1]
         eh, ah = (2.0 ** -17, 0.0) if self.dt == BF16 else (2.0 ** -22, 2.0 ** -25)   # the two halves of U and dU
+        eg, ag = 2.0 ** -24, (0.0 if self.dt == BF16 else 2.0 ** -47)                 # the three parts
         step = lambda n: (n / 16 + 16) * 2.0 ** -23
         out = {"Y": X @ W.t(), "U": torch.zeros(M, r).double(), "dX": dY @ W, "dA": torch.zeros(self.n, r, K).double(),
                "dB": torch.zeros(self.n, N, r).double()}
@@ -120,17 +121,18 @@ class Case:
             Ua = X[m] @ A[a].t()
             tU = step(K) * (X[m].abs() @ A[a].abs().t())
             dU = s[a] * (dY[m] @ B[a])
-            tdU = s[a] * step(N) * (dY[m].abs() @ B[a].abs()) + eh * dU.abs() + ah
-            tsU = s[a] * tU + eh * (s[a] * Ua).abs() + ah
+            rdU = s[a] * step(N) * (dY[m].abs() @ B[a].abs())
+            tdU, tsU = rdU + eh * dU.abs() + ah, s[a] * tU + eh * (s[a] * Ua).abs() + ah
+            gdU, gsU = rdU + eg * dU.abs() + ag, s[a] * tU + eg * (s[a] * Ua).abs() + ag
             out["U"][m], tol["U"][m] = Ua, tU
             out["Y"][m] += s[a] * Ua @ B[a].t()
             tol["Y"][m] += tsU @ B[a].abs().t() + step(K + 2 * r + 64) * (s[a] * Ua).abs() @ B[a].abs().t()
             out["dX"][m] += dU @ A[a]
             tol["dX"][m] += tdU @ A[a].abs() + step(N + 2 * r + 64) * dU.abs() @ A[a].abs()
             out["dA"][a] = dU.t() @ X[m]
-            tol["dA"][a] = tdU.t() @ X[m].abs() + step(2 * M) * (dU.abs().t() @ X[m].abs())
+            tol["dA"][a] = gdU.t() @ X[m].abs() + step(2 * M) * (dU.abs().t() @ X[m].abs())
             out["dB"][a] = s[a] * dY[m].t() @ Ua
-            tol["dB"][a] = dY[m].abs().t() @ tsU + step(2 * M) * (dY[m].abs().t() @ (s[a] * Ua).abs())
+            tol["dB"][a] = dY[m].abs().t() @ gsU + step(2 * M) * (dY[m].abs().t() @ (s[a] * Ua).abs())
         return out, tol
 
     def fwd(self, **k):
@@ -238,6 +240,23 @@ def test_a_single_adapter_and_none_at_all(M, N, K, r, n, rows):
                                             (200, 264, 384, 64, 3, "runs"), (520, 136, 256, 130, 4, "runs")])
 def test_types(M, N, K, r, n, rows, dt, out, dq):
     check(Case(M, N, K, r, n, rows, dt=dt, dq=dq), out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [8, 48, 100, 160])
+def test_small_fp16_gradients_keep_their_digits(r):
+    """dU of about 1e-5, under fp16's normal numbers, as early in training when B is near zero.  Two parts
+    of fp16 alone would be off by 2^-25 / 1e-5, three thousandths; 2^-18 is far above what an fp32 sum of 200
+    terms loses."""
+    c = Case(200, 136, 192, r, 3, "runs", dt=F16)
+    c.dY.mul_(1e-3)
+    c.B.mul_(1e-2)
+    ref, tol = c.reference()
+    _, dA, dB = c.bwd()
+    close("dA", dA, ref["dA"], tol["dA"])
+    close("dB", dB, ref["dB"], tol["dB"])
+    rel = lambda x, y: float((x.double().cpu() - y).norm() / y.norm())
+    assert rel(dA, ref["dA"]) <= 2.0 ** -18 and rel(dB, ref["dB"]) <= 2.0 ** -18
 
 
 @pytest.mark.gpu
