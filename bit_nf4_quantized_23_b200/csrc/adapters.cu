@@ -688,10 +688,11 @@ inline int32_t grad_ranks(int32_t r) { return (int32_t)round_up(r, grad_block(r)
 
 // Workspace, every piece 256-byte aligned:
 //   the lists; V2, 16-bit [M, 2R] (hi | lo of s U in the forward, of dU in the backward); U3 and dU3,
-//   16-bit [M, 3 Rg] (three parts of s U and of dU); partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
+//   16-bit [M, 3 Rg] (three parts of s U and of dU); split, fp32 partial outputs of a split reduction; partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
 //   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
 struct AdaptersWs {
-    size_t tok, n512, e512, n_grad, e_grad, v2, u3, du3, part, b8, dy8, total;
+    size_t tok, n512, e512, n_grad, e_grad, v2, u3, du3, part, split, b8, dy8, total;
+    size_t split_bytes;
     int32_t cap512, tiles64;
     int64_t tiles512;
 };
@@ -726,6 +727,8 @@ AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     size_t part = (size_t)std::max(part_splits(M, K, r), part_splits(M, N, r)) * M * Rn * 4;
     if (M <= kRowsMaxM) part = std::max(part, rows_workspace_bytes(M, N, K, r, n));
     w.part = piece(part);
+    w.split_bytes = std::max(M > kRowsMaxM ? adapters_split_bytes(M, N, K, false) : 0, adapters_split_bytes(M, N, K, true));
+    w.split = piece(w.split_bytes);
     w.b8 = piece(r % 8 ? (size_t)n * N * round_up(r, 8) * 2 : 0);
     w.dy8 = piece(N % 8 ? (size_t)M * round_up(N, 8) * 2 : 0);
     w.total = o;
@@ -877,10 +880,11 @@ qlora_status check_adapters(int64_t M, int64_t N, int64_t K, int32_t r, int32_t 
 
 // The fused GEMM of gemm_tc.cu over the tile lists: the forward (dx false) or dX.
 qlora_status adapters_gemm(const qlora_nf4_weight* w, const void* A0, int64_t ld0, int64_t M, const void* V2, const void* B1,
-                           int32_t b1_r, int32_t r, int32_t n, const AdapterLists& l, void* out, int32_t out_dtype,
-                           bool dx, cudaStream_t s) {
+                           int32_t b1_r, int32_t r, int32_t n, const AdapterLists& l, float* split_out, void* out,
+                           int32_t out_dtype, bool dx, cudaStream_t s) {
     TcGemmArgs a{};
     a.w = w; a.A0 = A0; a.a0_ld = ld0; a.A1 = V2; a.B1 = B1; a.b1_r = b1_r; a.Rpad = half_width(r); a.n_adapters = n;
+    a.split_out = split_out;
     a.p.M = M;
     a.p.Nout = dx ? w->K : w->N;
     a.p.ldo = a.p.Nout;
@@ -952,7 +956,8 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
         QLORA_TRY(launch_finish(u, FinishSource{}, M, r, l, scales, f16, s));
     }
     TimerScope t(QLORA_TIMER_FWD_MAIN, s);
-    return adapters_gemm(w, X, K, M, U2, B8, (int32_t)round_up(r, 8), r, n_adapters, l, Y, y_dtype, false, s);
+    return adapters_gemm(w, X, K, M, U2, B8, (int32_t)round_up(r, 8), r, n_adapters, l,
+                         reinterpret_cast<float*>(ws + lw.split), Y, y_dtype, false, s);
 }
 
 qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X, const void* dY, int64_t M,
@@ -1033,7 +1038,8 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
     qlora_status st = QLORA_OK;
     if (dX) {
         TimerScope t(QLORA_TIMER_DX_MAIN, s);
-        st = adapters_gemm(w, dY8, ldy, M, dU2, A_all, r, r, n_adapters, l, dX, dx_dtype, true, s);
+        st = adapters_gemm(w, dY8, ldy, M, dU2, A_all, r, r, n_adapters, l,
+                           reinterpret_cast<float*>(ws + lw.split), dX, dx_dtype, true, s);
     }
     if (st == QLORA_OK) {
         TimerScope t(QLORA_TIMER_LORA, g);

@@ -460,7 +460,11 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
     const int64_t n0 = nt * bn;                               // the pair's output column tile
     const int64_t nr0 = n0 + hb * (int64_t)rank;              // this CTA's output columns (forward: W rows)
     const uint32_t* const ad_list = MULTI ? p.ad.entry + mt * p.ad.cap * kAdEntry : nullptr;   // a pair's tile is kAdTile
-    const int ks0 = p.ksteps0, ktotal = p.ksteps0 + (MULTI ? (int)p.ad.count[mt] : 1) * p.ksteps1;
+    // MULTI: split blockIdx.y takes the steps kb0 .. kb0 + ks0 of the reduction over the frozen weight, the
+    // last split the adapters' steps too
+    const int kb0 = MULTI ? (int)blockIdx.y * p.split_steps : 0;
+    const int ks0 = MULTI ? min(p.split_steps, p.ksteps0 - kb0) : p.ksteps0;
+    const int ktotal = ks0 + (!MULTI ? p.ksteps1 : blockIdx.y + 1 == gridDim.y ? (int)p.ad.count[mt] * p.ksteps1 : 0);
     float* e4tab = reinterpret_cast<float*>(gbase + kPairOffE4);
     if (threadIdx.x < 256) e4tab[threadIdx.x] = e4m3_to_f32(threadIdx.x);
 
@@ -511,12 +515,13 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                 const uint32_t a_dst = sA + s * kPairAStage;
                 if (it < ks0) {
                     if (leader) ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * kPairAStage);
-                    ptx::tma_load_2d_pair(a_dst, &tmA0, it * 64, (int32_t)m0, lead_full_a + 8 * s);
+                    ptx::tma_load_2d_pair(a_dst, &tmA0, (kb0 + it) * 64, (int32_t)m0, lead_full_a + 8 * s);
                     ptx::mbar_arrive_expect_tx(bar_codes + 8 * s, DX ? kPairCodesStage : 32u * (uint32_t)hb);
                     if (!DX)
-                        ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, it * 32, (int32_t)nr0, bar_codes + 8 * s);
+                        ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, (kb0 + it) * 32, (int32_t)nr0,
+                                         bar_codes + 8 * s);
                     else
-                        ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, (int32_t)(nr0 / 2), it * 64,
+                        ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, (int32_t)(nr0 / 2), (kb0 + it) * 64,
                                          bar_codes + 8 * s);
                 } else {
                     const int j = MULTI ? je : it - ks0;
@@ -639,9 +644,10 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
         const bool in_tile = DX || t < hb;                    // forward rows past a narrow tile are never read
         // block of the step whose constants load next, moving by a fixed stride per group step
         // (forward: 2 blocks along the row; dX: 128 W rows down)
-        int64_t a_blk = DX ? ((int64_t)g * 64 + row) * blocks_per_row + (nr0 >> 6) + kc : (nr0 + t) * blocks_per_row + g;
+        int64_t a_blk = DX ? ((int64_t)(kb0 + g) * 64 + row) * blocks_per_row + (nr0 >> 6) + kc
+                           : (nr0 + t) * blocks_per_row + kb0 + g;
         const int64_t blk_step = DX ? 128 * blocks_per_row : 2;
-        int64_t a_n = (int64_t)g * 64 + row;                  // dX: the W row of that step
+        int64_t a_n = (int64_t)(kb0 + g) * 64 + row;                  // dX: the W row of that step
         auto const_load = [&](int step, bool& v, uint32_t& code, float& c2) {
             v = lane_ok && step < ks0 && (!DX || a_n < p.WN);
             code = 0;
@@ -719,7 +725,11 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                     ptx::tmem_ld_32x32b_x32(tmem + ((quad * 32u) << 16) + h * 256 + c * 32, v);
                     ptx::tmem_ld_wait();
                     if (m >= p.M) continue;
-                    store_row32(p, m, nb, nlim, v);
+                    if (MULTI && gridDim.y > 1)
+                        qlora::store_row32(static_cast<float*>(p.out) + blockIdx.y * p.split_elems, true, false, p.ldo, m, nb,
+                                           nlim, v);
+                    else
+                        store_row32(p, m, nb, nlim, v);
                 }
             }
         }
@@ -1269,7 +1279,7 @@ static qlora_status launch_one(const TcGemmArgs& a, cudaStream_t stream) {
 
 // The forward on CTA pairs: clusters of 2, one pair per 512 x 256 output tile.
 template <bool DX, bool MULTI>
-static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream) {
+static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream, int splits = 1) {
     static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
     auto kern = tc_gemm_nf4_pair<DX, MULTI>;
     if (!configured) {
@@ -1281,7 +1291,7 @@ static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream) {
     const int64_t pairs = ((a.p.Nout + bn - 1) / bn) * ((a.p.M + 511) / 512);
     if (2 * pairs > INT32_MAX) return QLORA_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.gridDim = dim3((unsigned)(2 * pairs), (unsigned)splits);
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = kPairAlloc;
     cfg.stream = stream;
@@ -1379,6 +1389,52 @@ static bool use_pairs_adapters(int64_t M, int64_t Nout, int bn) {
     if (M > 256) return true;
     const int64_t pair_waves = ((Nout + bn - 1) / bn + 73) / 74, waves = ((Nout + kBN - 1) / kBN + 147) / 148;
     return 2 * pair_waves <= 3 * waves;
+}
+
+// Splits of the reduction over the frozen weight, for batches whose pair tiles leave half of the GPU
+// idle: as many as fit on it, of at least 16 steps each, so that what a split saves (0.6 us a step)
+// outweighs the sum over the fp32 partial outputs.
+static int adapters_splits(int64_t M, int64_t Nout, int64_t red, int bn) {
+    const int64_t pairs = (M + 511) / 512 * ((Nout + bn - 1) / bn), steps = (red + 63) / 64;
+    const int64_t want = std::min<int64_t>(74 / pairs, steps / 16);
+    if (want < 2) return 1;
+    const int64_t per = (steps + want - 1) / want;
+    return (int)((steps + per - 1) / per);
+}
+
+size_t adapters_split_bytes(int64_t M, int64_t N, int64_t K, bool dx) {
+    const int64_t Nout = dx ? K : N;
+    const int bn = dx ? kBN : adapters_tile_width(M, N);
+    const int splits = use_pairs_adapters(M, Nout, bn) ? adapters_splits(M, Nout, dx ? N : K, bn) : 1;
+    return splits > 1 ? (size_t)splits * ((size_t)(M * Nout + 3) / 4 * 4) * sizeof(float) : 0;
+}
+
+// out[i] = the sum over the splits of partial[s][i], in order, rounded to the output type; four elements
+// per thread.
+__global__ void __launch_bounds__(256)
+sum_splits(const float* __restrict__ partial, int splits, int64_t stride, int64_t n, void* out, bool out_f32, bool f16) {
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < splits; ++s) {                        // the stride is a multiple of four: rows past n are scratch
+        const float4 x = *reinterpret_cast<const float4*>(partial + s * stride + i);
+        v.x = __fadd_rn(v.x, x.x);
+        v.y = __fadd_rn(v.y, x.y);
+        v.z = __fadd_rn(v.z, x.z);
+        v.w = __fadd_rn(v.w, x.w);
+    }
+    if (i + 4 <= n) {
+        if (out_f32) *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = v;
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) = make_uint2(pack16x2_rn(v.x, v.y, f16), pack16x2_rn(v.z, v.w, f16));
+        return;
+    }
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    for (int j = 0; i + j < n; ++j) {
+        if (out_f32) static_cast<float*>(out)[i + j] = e[j];
+        else static_cast<uint16_t*>(out)[i + j] = (uint16_t)to16_rn(e[j], f16);
+    }
 }
 
 // Splits of the reduction so that tiles x splits fills one wave of CTAs.
@@ -1508,7 +1564,24 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     a.p.err = device_error_word();
     if (!a.p.err) return QLORA_ERR_CUDA;
     if (a.n_adapters > 0) {
-        if (pair) return dx ? launch_pair<true, true>(a, stream) : launch_pair<false, true>(a, stream);
+        if (pair) {
+            const int splits = a.split_out ? adapters_splits(a.p.M, a.p.Nout, dx ? N : K, a.p.bn) : 1;
+            a.p.split_steps = (a.p.ksteps0 + splits - 1) / splits;
+            void* out = a.p.out;
+            const bool out_f32 = a.p.out_f32 != 0;
+            const int64_t n = a.p.M * a.p.Nout, blocks = (n + 1023) / 1024;
+            if (splits > 1) {
+                if (blocks > INT32_MAX) return QLORA_ERR_SHAPE;
+                a.p.split_elems = (n + 3) / 4 * 4;
+                a.p.out = a.split_out;
+            }
+            QLORA_TRY((dx ? launch_pair<true, true>(a, stream, splits) : launch_pair<false, true>(a, stream, splits)));
+            if (splits == 1) return QLORA_OK;
+            (void)launch_dependent(sum_splits, dim3((unsigned)blocks), dim3(256), 0, stream, (const float*)a.split_out, splits,
+                                   a.p.split_elems, n, out, out_f32, a.p.f16 != 0);
+            QLORA_CHECK_LAUNCH();
+            return QLORA_OK;
+        }
         if (bm == 256) return dx ? launch_one<2, true, true>(a, stream) : launch_one<2, false, true>(a, stream);
         return dx ? launch_one<1, true, true>(a, stream) : launch_one<1, false, true>(a, stream);
     }

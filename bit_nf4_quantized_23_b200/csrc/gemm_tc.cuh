@@ -40,6 +40,8 @@ struct TcGemmParams {
     uint32_t* err;
     NF4Tables tb;
     TileAdapters ad;        // MULTI kernels: the adapters of each token tile (ksteps1, b1_wrap per adapter)
+    int32_t split_steps;    // MULTI pairs: steps of ksteps0 per split of the reduction (grid y)
+    int64_t split_elems;    // elements between the splits' outputs
 };
 
 struct TcGemmArgs {
@@ -52,6 +54,7 @@ struct TcGemmArgs {
                             // ranks past b1_r read as zero; B needs b1_r % 8 == 0)
     int32_t b1_r;
     int32_t Rpad;           // LoRA rank padded to a multiple of 64 (32 too with n_adapters > 0)
+    float* split_out;       // one adapter per token: fp32 partial outputs, adapters_split_bytes, or NULL for none
     int32_t n_adapters;     // > 0: one adapter per token; B1 is B_all [n, N, b1_r] or A_all [n, b1_r, K] and p.ad is set
     TcGemmParams p;
     CUtensorMap tmA0, tmCodes, tmA1, tmB1;
@@ -59,6 +62,9 @@ struct TcGemmArgs {
 
 // Encodes the tensor maps and launches the forward (dx = false) or dX kernel.
 qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream);
+
+// Bytes of split_out that the forward (dx false) or dX with one adapter per token needs; 0 without splits.
+size_t adapters_split_bytes(int64_t M, int64_t N, int64_t K, bool dx);
 
 // Small-M forward (M <= 16): swap-AB fused dequant-GEMM, stream-K over
 // (tile, K-step) units with fp32 partial tiles and a fixup that adds the LoRA term.

@@ -221,6 +221,14 @@ def test_few_tokens(M, N, K, r, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n", [(150, 260, 4096, 8, 3), (70, 4163, 192, 20, 5), (400, 2112, 2112, 96, 4), (530, 136, 3008, 150, 2)])
+@pytest.mark.parametrize("dt,out", [(BF16, BF16), (F16, F32)])
+def test_few_tiles_and_a_long_reduction(M, N, K, r, n, dt, out):
+    """Products whose reduction is split over idle SMs and summed afterwards, odd output sizes among them."""
+    check(Case(M, N, K, r, n, "mixed", dt=dt), out)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,r,n,rows", [(600, 40, 64, 2, 9000, "mixed"), (4500, 72, 128, 8, 3, "runs"),
                                             (2100, 136, 64, 16, 700, "mixed"), (4097, 64, 64, 8, 2, "mixed")])
 def test_many_adapters_and_many_tokens(M, N, K, r, n, rows):
