@@ -388,8 +388,11 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
                 w[1] = ld_shared_v4(src + (16u ^ swz));
                 w[2] = ld_shared_v4(src + 4096u + swz);
                 w[3] = ld_shared_v4(src + 4096u + (16u ^ swz));
+                // The codes are in registers before the stage is given up: the loads above are still in flight
+                // here, and the copy that follows is the async proxy's, which an arrive alone does not order.
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_cempty + 8 * g);   // the codes are in registers
+                if (lane == 0) ptx::mbar_arrive(bar_cempty + 8 * g);
                 Lut lut;
                 // rows past N have a constant of 0 and so expand to zeros
                 float c1p = p.c1f ? k.c2a : __fadd_rn(__fmul_rn(e4m3_to_f32(k.ca), k.c2a), mu);

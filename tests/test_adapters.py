@@ -229,6 +229,41 @@ def test_few_tiles_and_a_long_reduction(M, N, K, r, n, dt, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n,dt", [(112, 28672, 8192, 64, 6, F16), (48, 8192, 8192, 16, 32, BF16), (4, 11008, 4096, 16, 4, BF16),
+                                          (700, 8192, 4096, 32, 9, BF16), (200, 4096, 11008, 64, 3, F16)])
+def test_full_size_layers_repeat_bit_for_bit(M, N, K, r, n, dt):
+    """Long runs of units through every ring, several times: any order of arrival that reaches a result
+    shows as a difference, and one run is compared with the formula in fp64 on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    rnd = lambda *shape, std=1.0, to=dt: (torch.randn(*shape, generator=g, device="cuda") * std).to(to)
+    w = q4.qlora_quantize_nf4_dq(rnd(N, K, std=0.02, to=BF16), compute_dtype=dt, double_quant=M % 8 != 0)
+    X, dY, A, B = rnd(M, K), rnd(M, N, std=0.1), rnd(n, r, K, std=K ** -0.5), rnd(n, N, r, std=0.05)
+    idx = torch.randint(-1, n, (M,), generator=g, device="cuda").int().sort().values
+    scales = torch.rand(n, generator=g, device="cuda") + 0.5
+    runs = []
+    for i in range(5):
+        Y, U = q4.qlora_linear_fwd_adapters(w, X, A, B, idx, scales)
+        runs.append((Y, U) + q4.qlora_linear_bwd_adapters(w, X, dY, A, B, idx, scales, U_saved=U))
+    for later in runs[1:]:
+        for a, b in zip(runs[0], later):
+            assert torch.equal(a, b)
+    W = q4.qlora_dequantize(w).double()
+    Yr, dXr = X.double() @ W.t(), dY.double() @ W
+    for a in range(n):
+        m = (idx == a).nonzero()[:, 0]
+        Yr[m] += float(scales[a]) * (X[m].double() @ A[a].double().t()) @ B[a].double().t()
+        dXr[m] += float(scales[a]) * (dY[m].double() @ B[a].double()) @ A[a].double()
+    # sums of K or N products, each accumulation step off by 2^-23 of the sum of magnitudes, which for these
+    # inputs is below sqrt(count) times the result's own scale; half a step of the type on top
+    for name, got, ref, count in (("Y", runs[0][0], Yr, K), ("dX", runs[0][2], dXr, N)):
+        scale = float(ref.std())
+        off = (got.double() - ref).abs()
+        room = torch.finfo(dt).eps / 2 * ref.abs() + (count / 16 + 16) * 2.0 ** -23 * count ** 0.5 * scale + 2.0 ** -15 * scale
+        assert torch.all(off <= room), (name, float((off / room).max()))
+    assert q4.qlora_read_device_errors(clear=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,r,n,rows", [(600, 40, 64, 2, 9000, "mixed"), (4500, 72, 128, 8, 3, "runs"),
                                             (2100, 136, 64, 16, 700, "mixed"), (4097, 64, 64, 8, 2, "mixed")])
 def test_many_adapters_and_many_tokens(M, N, K, r, n, rows):
