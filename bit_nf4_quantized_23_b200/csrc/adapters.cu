@@ -444,7 +444,10 @@ finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, i
 // of N = RB for each part when that exceeds 256); the epilogue adds the parts in fp32.
 // Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 zero the rows of other
 // tokens in tiles that the adapter shares, then run the epilogue.
+// Every 32 token tiles the accumulators are added to the output and begun anew: the tensor cores' fp32
+// sums lose about 2^-27 of themselves at each 16-wide step, one way, which a long batch would notice.
 constexpr int kGradThreads = 192;
+constexpr int kGradFlush = 32;
 
 struct GradParams {
     int64_t M, K, N;
@@ -467,7 +470,7 @@ __host__ __device__ inline GradLayout grad_layout(uint32_t stages, uint32_t v_by
     GradLayout l;
     l.off_v = stages * kStage16K;
     l.off_bars = l.off_v + stages * v_bytes;
-    l.off_slot = l.off_bars + (3 * stages + 1) * 8;
+    l.off_slot = l.off_bars + (3 * stages + 2) * 8;
     l.off_abort = l.off_slot + 4;
     l.alloc = l.off_abort + 4 + 1024;
     return l;
@@ -485,7 +488,7 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     const int S = (int)p.stages;
     const uint32_t sS = base, sV = base + lay.off_v;
     const uint32_t bar_full = base + lay.off_bars, bar_ready = bar_full + 8 * S, bar_empty = bar_ready + 8 * S;
-    const uint32_t bar_acc = bar_empty + 8 * S;
+    const uint32_t bar_acc = bar_empty + 8 * S, bar_flushed = bar_acc + 8;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + lay.off_slot);
     volatile int* abort = reinterpret_cast<volatile int*>(gbase + lay.off_abort);
 
@@ -504,6 +507,7 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
         ptx::mbar_init(bar_acc, 1);
+        ptx::mbar_init(bar_flushed, 4);
         *abort = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
@@ -548,10 +552,13 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         const uint32_t idesc =
             ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, side ? 3 * p.RB : p.RB, 1, 1), p.f16 != 0);
         int s = 0;
-        uint32_t ph = 0;
+        uint32_t ph = 0, acc_ph = 0;                          // phase of bar_acc that the next commit completes
         bool ok = true;
         for (int i = 0; i < nt && ok; ++i) {
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_ready + 8 * s, ph, abort, p.err));
+            const bool fresh = i % kGradFlush == 0;
+            bool w = true;
+            if (fresh && i > 0) w = ptx::mbar_wait(bar_flushed, (uint32_t)(i / kGradFlush - 1) & 1u, abort, p.err);
+            ok = __all_sync(0xffffffffu, w && ptx::mbar_wait(bar_ready + 8 * s, ph, abort, p.err));
             if (!ok) break;
             ptx::tc_fence_after();
             if (ptx::elect_one_sync()) {
@@ -562,20 +569,70 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     for (int part = 0; part < (side ? 1 : 3); ++part)
                         ptx::mma_bf16_ss(tmem + (uint32_t)(part * p.RB), ad_desc,
                                          ptx::smem_desc_sw128(b_base + part * (p.RB / 64) * 8192 + kk * 2048, 8192, 1024),
-                                         idesc, (i | kk) != 0 ? 1u : 0u);
+                                         idesc, (fresh && kk == 0) ? 0u : 1u);
                 }
                 ptx::mma_commit(bar_empty + 8 * s);
+                if ((i + 1) % kGradFlush == 0 && i + 1 < nt) ptx::mma_commit(bar_acc);
             }
             __syncwarp();
+            if ((i + 1) % kGradFlush == 0 && i + 1 < nt) acc_ph ^= 1u;
             if (++s == S) { s = 0; ph ^= 1u; }
         }
         if (ptx::elect_one_sync()) {
             ptx::mma_commit(bar_acc);
-            if (*abort) ptx::mbar_wait_drain(bar_acc, 0);   // issued MMAs finish before TMEM is freed
+            if (*abort) ptx::mbar_wait_drain(bar_acc, acc_ph);   // issued MMAs finish before TMEM is freed
         }
         __syncwarp();
     } else {
         const int t = threadIdx.x - 64, row = t & 63, half = t >> 6;
+        const uint32_t quad = (uint32_t)(warp & 3);
+        const int64_t orow = row0 + quad * 32 + lane;
+        const bool in = orow < (is_a ? p.K : p.N);
+        const int j0 = (int)blockIdx.z * p.RB, nj = min(p.r - j0, p.RB);
+        float* const dst = is_a ? p.dA + ((int64_t)ad * p.r + j0) * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r + j0;
+        const int64_t pitch = is_a ? p.K : 1;                 // between a thread's ranks
+        const bool vec = !is_a && p.r % 4 == 0;
+        const float down = p.f16 ? 1.f / kPartScale : 1.f;
+        // the accumulators of piece f of the token tiles, stored (f = 0) or added to what the thread stored
+        auto flush = [&](int f) -> bool {
+            const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, (uint32_t)f & 1u, abort, p.err));
+            if (!acc_ok) return false;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c * 16 < nj; ++c) {
+                float v[16];
+                if (nt > 0) {
+                    uint32_t part[3][16];
+#pragma unroll
+                    for (int w = 0; w < 3; ++w)
+                        ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + (uint32_t)(w * p.RB + c * 16), part[w]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        v[q] = __fmaf_rn(__fmaf_rn(__uint_as_float(part[2][q]), down, __uint_as_float(part[1][q])), down,
+                                         __uint_as_float(part[0][q]));
+                } else {                                      // no token has this adapter
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] = 0.f;
+                }
+                if (!in) continue;
+                float* at = dst + (int64_t)c * 16 * pitch;
+                if (f > 0)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (c * 16 + q < nj) v[q] = __fadd_rn(at[q * pitch], v[q]);
+                if (vec) {
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4)
+                        if (c * 16 + q < nj) *reinterpret_cast<float4*>(at + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (c * 16 + q < nj) at[q * pitch] = v[q];
+                }
+            }
+            return true;
+        };
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -604,48 +661,15 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             if (lane == 0) ptx::mbar_arrive(bar_ready + 8 * s);
             e = next;
             if (++s == S) { s = 0; ph ^= 1u; }
-        }
-        const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
-        ptx::tc_fence_after();
-        if (acc_ok) {
-            const uint32_t quad = (uint32_t)(warp & 3);
-            const int64_t orow = row0 + quad * 32 + lane;
-            const bool in = orow < (is_a ? p.K : p.N);
-            const int j0 = (int)blockIdx.z * p.RB, nj = min(p.r - j0, p.RB);
-            float* dst = is_a ? p.dA + ((int64_t)ad * p.r + j0) * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r + j0;
-            const bool vec = !is_a && p.r % 4 == 0;
-            const float down = p.f16 ? 1.f / kPartScale : 1.f;
-#pragma unroll 1
-            for (int c = 0; c * 16 < nj; ++c) {
-                float v[16];
-                if (nt > 0) {
-                    uint32_t part[3][16];
-#pragma unroll
-                    for (int w = 0; w < 3; ++w)
-                        ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + (uint32_t)(w * p.RB + c * 16), part[w]);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        v[q] = __fmaf_rn(__fmaf_rn(__uint_as_float(part[2][q]), down, __uint_as_float(part[1][q])), down,
-                                         __uint_as_float(part[0][q]));
-                } else {                                      // no token has this adapter
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] = 0.f;
-                }
-                if (!in) continue;
-#pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    const int j = c * 16 + q;
-                    if (vec) {
-                        if (j < nj) *reinterpret_cast<float4*>(dst + j) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (j + u < nj) dst[is_a ? (int64_t)(j + u) * p.K : j + u] = v[q + u];
-                    }
-                }
+            if ((i + 1) % kGradFlush == 0 && i + 1 < nt) {
+                ok = flush(i / kGradFlush);
+                if (!ok) break;
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_flushed);
             }
         }
+        if (ok) (void)flush(nt > 0 ? (nt - 1) / kGradFlush : 0);
     }
 
     ptx::tc_fence_before();
@@ -698,12 +722,13 @@ struct AdaptersWs {
 };
 
 // Splits of the reduction of U or dU: two CTAs for each of 148 SMs (a count fixed here, so that the
-// workspace does not depend on the current device) while each has at least two steps of 64, rounded so
-// that no split is empty.
+// workspace does not depend on the current device) while each has at least two steps of 64, and no more
+// than 32 steps each: the tensor cores' fp32 sums lose about 2^-27 of themselves at every 16-wide step,
+// one way.  Rounded so that no split is empty.
 int part_splits(int64_t M, int64_t red, int32_t r) {
     const int64_t tiles = (M + kPartTile - 1) / kPartTile, steps = (red + 63) / 64;
     const int64_t most = r <= 128 ? 2 * 148 : 148;            // CTAs that run together
-    const int64_t want = std::max<int64_t>(1, std::min(most / tiles, steps / 2));
+    const int64_t want = std::max<int64_t>((steps + 31) / 32, std::min(most / tiles, steps / 2));
     const int64_t per = (steps + want - 1) / want;
     return (int)((steps + per - 1) / per);
 }
@@ -768,13 +793,9 @@ qlora_status launch_pad_rows(const void* in, int64_t rows, int64_t cols, void* o
 
 template <bool V_MN>
 qlora_status launch_part(const CUtensorMap& tmS, const CUtensorMap& tmV, PartParams& p, int splits, cudaStream_t s) {
-    static bool configured = false;
+    static std::atomic<uint64_t> configured{0};
     auto kern = tc_part_gemm<V_MN>;
-    if (!configured) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
+    if (!allow_smem(configured, (const void*)kern, (int)kMaxSmem)) return QLORA_ERR_CUDA;
     // two CTAs per SM up to 128 ranks: three S stages and the rest of 108 KiB for V tiles, of which a tile of
     // many adapters takes many per S tile
     p.s_stages = 3;
@@ -833,13 +854,8 @@ qlora_status launch_finish(const FinishSource& s0, const FinishSource& s1, int64
 qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M, int64_t N, int64_t K, int32_t r,
                           int32_t n, const void* dU3, const void* U3, const AdapterLists& l, bool f16, float* dA,
                           float* dB, cudaStream_t s) {
-    static bool configured = false;
-    if (!configured) {
-        if (cudaFuncSetAttribute(tc_adapter_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) !=
-            cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0};
+    if (!allow_smem(configured, (const void*)tc_adapter_grads, (int)kMaxSmem)) return QLORA_ERR_CUDA;
     GradParams p{};
     const int32_t RB = grad_block(r), Rg = grad_ranks(r);
     p.M = M; p.K = K; p.N = N; p.r = r; p.RB = RB;
@@ -1019,8 +1035,17 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
     }
     // The adapter gradients run beside dX on the low-priority side stream and fill the SMs that its last
     // wave of tiles leaves idle.  Below about ten microseconds of dX the fork and join take longer on the
-    // host than they save on the GPU, and the two run in turn.
-    const bool forked = dX && (double)M * (double)N * (double)K >= 5e9;
+    // host than they save on the GPU, and the two run in turn.  So they do in a capture: the side stream is
+    // one for all threads, and one thread's capture must not take in another's launches.
+    bool forked = dX && (double)M * (double)N * (double)K >= 5e9;
+    if (forked) {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return QLORA_ERR_CUDA;
+        }
+        forked = capture == cudaStreamCaptureStatusNone;
+    }
     cudaStream_t g = forked ? side_stream() : s;
     cudaEvent_t join = nullptr;
     if (forked) {

@@ -12,7 +12,9 @@
 //
 // Work units are 256 rows x 64 of K; the units, tile major, are cut into equal contiguous ranges, one
 // per CTA (one CTA per SM), and every (tile, CTA) piece is a segment accumulated in TMEM and written as
-// an fp32 partial tile to slot tile + CTA.  rows_finish_U sums the adapters' tiles to U, tc_rows_fixup
+// an fp32 partial tile to slot tile + CTA.  The tensor cores' fp32 sums lose about 2^-27 of themselves at
+// each step, one way, so tiles of A_all rows, whose U must keep fp32 digits for the gradients, are cut
+// into pieces of 1024 of K, each with slots of its own.  rows_finish_U sums the adapters' tiles to U, tc_rows_fixup
 // the others, adds the adapter term s_a U B_a^T on the tensor cores and writes Y.
 //
 // The expansion of the codes bounds the kernel (byte permutes, about three ALU operations a weight on a
@@ -20,8 +22,8 @@
 // weights per handshake, the codes' stages are freed as soon as they are in registers, and a unit takes
 // four MMAs and two copies.
 // Roles (608 threads): warp 0 TMA of the tokens (and A_all rows), warp 1 TMEM owner + MMA issuer, warp 2
-// TMA of the codes (a warp of its own: behind the token ring the codes came a unit too late, 77 against
-// {CODES} us at W[28672, 8192] and 112 tokens), warps 3-18 four groups of producer warps that take units in
+// TMA of the codes (a warp of its own: behind the token ring the codes came a unit too late, 106 against
+// 100 us a call at W[28672, 8192] and 112 tokens), warps 3-18 four groups of producer warps that take units in
 // turn; groups 0 and 1 also run the epilogues of even and odd segments.
 //
 // A parity wait tells apart only neighbouring phases, so no role may come to a barrier two phases
@@ -45,6 +47,7 @@ constexpr int kMaxCtas = 256;
 constexpr uint32_t kRowStage = 256 * 128;         // 256 rows x 64 16-bit elements
 constexpr uint32_t kCodeStage = 256 * 32;         // their packed codes, 32-byte swizzled
 constexpr uint32_t kMaxSmem = 227 * 1024;
+constexpr int kPiece = 16;                        // units of a piece of a tile of A_all rows
 constexpr int kPrefetch = 2;                      // block constants are loaded this many units (of the group) ahead
 
 struct RowsLayout {
@@ -80,12 +83,19 @@ struct RowsParams {
     int32_t f16;
     uint32_t nt, x_stages;
     float* partial;                               // [tiles + CTAs][nt][256]
+    int2* piece_ctas;                             // first and last CTA of each piece of A_all rows
     int32_t* meta;                                // [0] adapters in use, [1 + m] place of token m's adapter among them, or -1
     uint32_t* err;
     NF4Tables tb;
 };
 
 __host__ __device__ __forceinline__ int64_t range_begin(int64_t b, int64_t units, int64_t G) { return b * units / G; }
+
+// Slots are counted in pieces: a tile of A_all rows has pieces_of(S) of them, a W_hat tile one.
+__host__ __device__ __forceinline__ int pieces_of(int S) { return (S + kPiece - 1) / kPiece; }
+__device__ __forceinline__ int piece_at(int tile, int step, int u_tiles, int pieces) {
+    return tile < u_tiles ? tile * pieces + step / kPiece : u_tiles * pieces + (tile - u_tiles);
+}
 
 // Adapters whose rows share a tile of A_all rows.
 __host__ __device__ __forceinline__ int adapters_per_tile(int rp) { return 256 / rp; }
@@ -174,6 +184,7 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     if (tid < 128) {
         const int place = a >= 0 ? place_of(first) : -1;
         if (a >= 0 && first == tid) list[place] = a;
+        ids[tid] = place;                                     // from here on the token's place among the adapters
         if (blockIdx.x == 0) {
             if (tid < p.M) p.meta[1 + tid] = place;
             if (tid == 0) p.meta[0] = used;
@@ -189,6 +200,7 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     const int n = (int)(range_begin(blockIdx.x + 1, units, gridDim.x) - u0);
     const int t0 = (int)(u0 / S), step0 = (int)(u0 - (int64_t)t0 * S);
     const int nu = (int)max((int64_t)0, min((int64_t)n, (int64_t)u_tiles * S - u0));   // units of A_all rows
+    const int pieces = pieces_of(S), piece0 = piece_at(t0, step0, u_tiles, pieces);   // segment s is piece piece0 + s
 
     if (warp == 0) {
         // unit i: X into token slot i % XS once the MMA that read it before has completed, with it an
@@ -260,9 +272,9 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
                                              ptx::mbar_wait(bar_bfull + 8 * g, gph, abort, p.err));
             if (!ok) break;
             ptx::tc_fence_after();
-            const bool last = (step + 1 == S) || (i == n - 1);
+            const bool is_w = i >= nu;
+            const bool last = (step + 1 == S) || (i == n - 1) || (!is_w && (step + 1) % kPiece == 0);
             if (ptx::elect_one_sync()) {
-                const bool is_w = i >= nu;
                 const uint64_t ad = x_sw + (uint32_t)xs * (lay.x_stage >> 4);
                 const uint64_t bd = (is_w ? b_none : b_sw) + (uint32_t)g * (kRowStage >> 4);
                 const uint32_t bk = is_w ? (2u * 256 * 16) >> 4 : 32u >> 4, d = tmem + 256u * acc;
@@ -339,22 +351,36 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
         }
 
         int epi_seg = g < 2 ? g : INT_MAX / 2;                // next segment whose epilogue is this group's
-        const int last_seg = (int)((u0 + n - 1) / S) - t0;
+        const int t_end = (int)((u0 + n - 1) / S);
+        const int last_seg = piece_at(t_end, (int)(u0 + n - 1 - (int64_t)t_end * S), u_tiles, pieces) - piece0;
         auto epilogue = [&](int seg) -> bool {
             const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_accfull + 8 * g, (uint32_t)(seg >> 1) & 1u,
                                                                     abort, p.err));
             if (!ok) return false;
             ptx::tc_fence_after();
+            const int piece = piece0 + seg;
             const uint32_t quad = (uint32_t)(warp & 3);       // TMEM lanes that the warp reaches: its tokens
             const int m = (int)(quad * 32u) + lane;
+            uint32_t lo = 0, hi = m < p.M ? 256 : 0;          // columns that the token needs
+            if (piece < u_tiles * pieces) {                   // of A_all rows only its own adapter's
+                const int q = ids[m] - piece / pieces * per_tile;
+                lo = (uint32_t)(q * p.rp);
+                hi = hi && ids[m] >= 0 && q >= 0 && q < per_tile ? lo + (uint32_t)p.r : 0;
+            }
+            if (t == 0 && piece < u_tiles * pieces) {         // note the piece's first and last CTA for rows_finish_U
+                const int tile = piece / pieces, k = piece - tile * pieces;
+                const int64_t begin = (int64_t)tile * S + k * kPiece, end = (int64_t)tile * S + min(S, (k + 1) * kPiece);
+                if (begin >= u0) p.piece_ctas[piece].x = (int32_t)blockIdx.x;
+                if (end <= u0 + n) p.piece_ctas[piece].y = (int32_t)blockIdx.x;
+            }
             if ((int)(quad * 32u) < p.M) {
-                float* dst = p.partial + ((int64_t)(t0 + seg + blockIdx.x) * p.nt + m) * 256;
+                float* dst = p.partial + ((int64_t)(piece0 + seg + blockIdx.x) * p.nt + m) * 256;
 #pragma unroll 1
                 for (uint32_t c = 0; c < 256; c += 32) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(tmem + ((quad * 32u) << 16) + 256u * (uint32_t)g + c, v);
                     ptx::tmem_ld_wait();
-                    if (m < p.M) {
+                    if (c < hi && c + 32 > lo) {
                         uint4* d4 = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) d4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -370,7 +396,7 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
         bool ok = true;
         uint32_t cph = 0, ph = 1;
         for (int i = g; i < n && ok; i += kGroups) {
-            const int seg = cur.tile - t0;
+            const int seg = piece_at(cur.tile, cur.step, u_tiles, pieces) - piece0;
             while (epi_seg < seg && ok) { ok = epilogue(epi_seg); epi_seg += 2; }
             if (!ok) break;
             const Consts k = q[0];
@@ -428,15 +454,15 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
     }
 }
 
-// The CTAs whose ranges hold the units of a tile: unit u belongs to the largest b with b units / G <= u,
-// that is b units < (u + 1) G.
-__device__ __forceinline__ int2 tile_span(int tile, int steps, int64_t units, int G) {
-    const int64_t u = (int64_t)tile * steps;
-    return make_int2((int)(((u + 1) * G - 1) / units), (int)(((u + steps) * G - 1) / units));
+// The CTAs whose ranges hold the units u .. u + count - 1: unit u belongs to the largest b with
+// b units / G <= u, that is b units < (u + 1) G.
+__device__ __forceinline__ int2 unit_span(int64_t u, int count, int64_t units, int G) {
+    return make_int2((int)(((u + 1) * G - 1) / units), (int)(((u + count) * G - 1) / units));
 }
 
 struct FixParams {
     const float* partial;
+    const int2* piece_ctas;
     const int32_t* meta;
     const int32_t* idx;
     const float* scales;
@@ -445,6 +471,7 @@ struct FixParams {
     void* out;
     int64_t N;
     int32_t M, r, R, rp, steps, w_tiles, G;
+    int32_t all_pieces;       // of A_all rows, at most
     uint32_t nt;
     int32_t out_f32, f16;
     uint32_t* err;
@@ -454,25 +481,37 @@ struct FixParams {
 // halves of s_a U[m, j] in the 16-bit compute type, U2 [M, 2R]: zeros for j >= r and without an adapter.
 __global__ void __launch_bounds__(128)
 rows_finish_U(FixParams p) {
+    __shared__ int2 ctas[128];                                // of the first pieces: loaded with the tokens' places
     grid_dependency_wait();
     allow_dependents();
     const int i = (int)(blockIdx.x * 128 + threadIdx.x), m = i / p.R, j = i - m * p.R;
+    const int place = m < p.M ? p.meta[1 + m] : -1, adapter = m < p.M ? p.idx[m] : -1;
+    if ((int)threadIdx.x < p.all_pieces) ctas[threadIdx.x] = p.piece_ctas[threadIdx.x];
+    __syncthreads();
     if (m >= p.M) return;
-    const int place = p.meta[1 + m], per_tile = adapters_per_tile(p.rp);
-    const int u_tiles = (p.meta[0] + per_tile - 1) / per_tile;
     float v = 0.f, sv = 0.f;
     if (place >= 0 && j < p.r) {
-        const float sc = __ldg(p.scales + p.idx[m]);
-        const int t = place / per_tile, row = (place - t * per_tile) * p.rp + j;
+        const float sc = __ldg(p.scales + adapter);
+        const int per_tile = adapters_per_tile(p.rp), t = place / per_tile, row = (place - t * per_tile) * p.rp + j;
         const int64_t slot_floats = (int64_t)p.nt * 256;
-        const int2 sp = tile_span(t, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
-        const float* src = p.partial + (int64_t)(t + sp.x) * slot_floats + (int64_t)m * 256 + row;
-        for (int b = sp.x; b <= sp.y; b += 8, src += 8 * slot_floats) {
-            float x[8];
+        const int pieces = pieces_of(p.steps), first = t * pieces;
+        const float* src = p.partial + (int64_t)first * slot_floats + (int64_t)m * 256 + row;
+        for (int k0 = 0; k0 < pieces; k0 += 4) {              // four pieces' first three slots in flight
+            int2 c[4];
+            float x[4][3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = b + e <= sp.y ? src[e * slot_floats] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+                const int k = k0 + e;
+                c[e] = k >= pieces ? make_int2(0, -1) : first + k < 128 ? ctas[first + k] : p.piece_ctas[first + k];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v = __fadd_rn(v, x[e]);
+                for (int b = 0; b < 3; ++b) x[e][b] = c[e].x + b <= c[e].y ? src[(k + c[e].x + b) * slot_floats] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int b = 0; b < 3; ++b) v = __fadd_rn(v, x[e][b]);
+                for (int b = c[e].x + 3; b <= c[e].y; ++b) v = __fadd_rn(v, src[(k0 + e + b) * slot_floats]);
+            }
         }
         sv = __fmul_rn(sc, v);
     }
@@ -625,7 +664,8 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         const int m = (int)(quad * 32u) + lane, col0 = (int)(blockIdx.x & 3u) * 64;
         const int per_tile = adapters_per_tile(p.rp), u_tiles = (used + per_tile - 1) / per_tile;
         const int tile = u_tiles + (int)(blockIdx.x >> 2);
-        const int2 sp = tile_span(tile, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
+        const int2 sp = unit_span((int64_t)tile * p.steps, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
+        const int slot0 = u_tiles * pieces_of(p.steps) + (tile - u_tiles) + sp.x;
         const bool has = m < p.M && p.meta[1 + m] >= 0;
         const int64_t slot_floats = (int64_t)p.nt * 256;
         const bool live = (int)(quad * 32u) < p.M;
@@ -633,7 +673,7 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0.f;
         if (m < p.M) {
-            const float* src = p.partial + (int64_t)(tile + sp.x) * slot_floats + (int64_t)m * 256 + col0;
+            const float* src = p.partial + (int64_t)slot0 * slot_floats + (int64_t)m * 256 + col0;
             for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
                 float4 v[16];
 #pragma unroll
@@ -680,12 +720,17 @@ inline uint32_t token_tile(int64_t M) { return (uint32_t)((M + 7) / 8 * 8); }
 
 }  // namespace
 
-// meta [1 + 128] int32, then the partial tiles of every W tile and of the tiles of A_all rows that M
-// tokens can use, plus one for each CTA boundary.
-size_t rows_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n_adapters) {
+// Pieces of A_all rows that M tokens can use.
+static int64_t u_pieces(int64_t M, int64_t K, int32_t r, int64_t n_adapters) {
     const int64_t per_tile = adapters_per_tile(adapter_rows(r));
-    const int64_t tiles = (N + 255) / 256 + (std::min(M, n_adapters) + per_tile - 1) / per_tile;
-    return 1024 + (size_t)(tiles + kMaxCtas) * token_tile(M) * 256 * sizeof(float);
+    return (std::min(M, n_adapters) + per_tile - 1) / per_tile * pieces_of((int)(K / 64));
+}
+
+// meta [1 + 128] int32 in 1 KiB, the pieces' CTAs, then the partial tiles: one slot for each piece and W
+// tile and one for each CTA boundary.
+size_t rows_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n_adapters) {
+    const int64_t pieces = u_pieces(M, K, r, n_adapters), slots = (N + 255) / 256 + pieces + kMaxCtas;
+    return 1024 + align_up((size_t)pieces * 8, 256) + (size_t)slots * token_tile(M) * 256 * sizeof(float);
 }
 
 qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
@@ -695,12 +740,10 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return QLORA_ERR_CUDA;
-    static bool configured = false;
-    if (!configured) {
-        if (cudaFuncSetAttribute(tc_rows_nf4, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
+    static std::atomic<uint64_t> configured{0}, fix_configured{0};
+    if (!allow_smem(configured, (const void*)tc_rows_nf4, (int)kMaxSmem) ||
+        !allow_smem(fix_configured, (const void*)tc_rows_fixup, (int)kMaxSmem))
+        return QLORA_ERR_CUDA;
     RowsParams p{};
     p.M = (int32_t)a.M; p.r = a.r;
     p.rp = adapter_rows(a.r);
@@ -716,7 +759,9 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     const RowsLayout lay = rows_layout(p.nt, p.x_stages);
     if (lay.alloc > kMaxSmem) return QLORA_ERR_UNSUPPORTED;
     p.meta = static_cast<int32_t*>(a.workspace);
-    p.partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + 1024);
+    p.piece_ctas = reinterpret_cast<int2*>(static_cast<char*>(a.workspace) + 1024);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + 1024 +
+                                         align_up((size_t)u_pieces(a.M, K, a.r, a.n_adapters) * 8, 256));
     p.tb = host_tables(w->codebook);
     p.err = device_error_word();
     if (!p.err) return QLORA_ERR_CUDA;
@@ -733,18 +778,13 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     (void)launch_dependent(tc_rows_nf4, dim3((unsigned)G), dim3(kThreads), lay.alloc, stream, tmCodes, tmX, tmA, p);
     QLORA_CHECK_LAUNCH();
     FixParams f{};
-    f.partial = p.partial; f.meta = p.meta; f.idx = a.idx; f.scales = a.scales; f.U = a.U; f.out = a.out; f.N = N;
+    f.partial = p.partial; f.piece_ctas = p.piece_ctas; f.meta = p.meta; f.idx = a.idx; f.scales = a.scales; f.U = a.U; f.out = a.out; f.N = N;
     f.U2 = static_cast<uint16_t*>(a.U2);
     f.M = p.M; f.r = p.r; f.R = a.R; f.rp = p.rp; f.steps = p.steps; f.w_tiles = p.w_tiles; f.G = (int32_t)G;
+    f.all_pieces = (int32_t)u_pieces(a.M, K, a.r, a.n_adapters);
     f.nt = p.nt; f.out_f32 = a.out_f32; f.f16 = p.f16; f.err = p.err;
     (void)launch_dependent(rows_finish_U, dim3((unsigned)((f.M * f.R + 127) / 128)), dim3(128), 0, stream, f);
     QLORA_CHECK_LAUNCH();
-    static bool fix_configured = false;
-    if (!fix_configured) {
-        if (cudaFuncSetAttribute(tc_rows_fixup, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        fix_configured = true;
-    }
     CUtensorMap tmU2, tmB;
     if (!make_tmap_2d(&tmU2, true, a.U2, 2 * a.R, a.M, 4 * a.R, 64, 128, true)) return QLORA_ERR_CUDA;
     if (!make_tmap_2d(&tmB, true, a.B, a.ldb, (uint64_t)a.n_adapters * N, a.ldb * 2, 64, 64, true)) return QLORA_ERR_CUDA;

@@ -1261,13 +1261,9 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, 
 template <int NUM_ACC, bool DX, bool MULTI>
 static qlora_status launch_one(const TcGemmArgs& a, cudaStream_t stream) {
     using L = Layout<NUM_ACC>;
-    static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
+    static std::atomic<uint64_t> configured{0};
     auto kern = tc_gemm_nf4<NUM_ACC, DX, MULTI>;
-    if (!configured) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kAlloc) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
+    if (!allow_smem(configured, (const void*)kern, (int)L::kAlloc)) return QLORA_ERR_CUDA;
     const int64_t tiles = ((a.p.Nout + kBN - 1) / kBN) * ((a.p.M + L::kBM - 1) / L::kBM);
     if (tiles > INT32_MAX) return QLORA_ERR_SHAPE;
     const dim3 grid((unsigned)tiles);
@@ -1280,13 +1276,9 @@ static qlora_status launch_one(const TcGemmArgs& a, cudaStream_t stream) {
 // The forward on CTA pairs: clusters of 2, one pair per 512 x 256 output tile.
 template <bool DX, bool MULTI>
 static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream, int splits = 1) {
-    static bool configured = false;   // attribute set once per instantiation (idempotent, so races are benign)
+    static std::atomic<uint64_t> configured{0};
     auto kern = tc_gemm_nf4_pair<DX, MULTI>;
-    if (!configured) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairAlloc) != cudaSuccess)
-            return QLORA_ERR_CUDA;
-        configured = true;
-    }
+    if (!allow_smem(configured, (const void*)kern, (int)kPairAlloc)) return QLORA_ERR_CUDA;
     const int bn = DX ? kBN : a.p.bn;
     const int64_t pairs = ((a.p.Nout + bn - 1) / bn) * ((a.p.M + 511) / 512);
     if (2 * pairs > INT32_MAX) return QLORA_ERR_SHAPE;

@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/qlora.h"
@@ -53,6 +54,18 @@ qlora_status check_lora(int64_t M, int32_t r, float alpha);                // to
 qlora_status check_out_dtype(int32_t dt, const qlora_nf4_weight* w);      // fp32 or the compute dtype
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Host side: raises a kernel's limit of dynamic shared memory, once per device (the attribute belongs to
+// the device).  `done` has a bit per device; setting it twice is harmless.
+inline bool allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Host side: the low-priority side stream of the current device, on which the backward's adapter
 // gradients run beside dX (api.cu; nullptr on failure).

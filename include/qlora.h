@@ -292,6 +292,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const void* X, const vo
  *   workspace   at least qlora_adapters_workspace_size bytes; its contents need not
  *               start at any value, and calls that overlap on the GPU need their own.
  * Neither other tokens nor other adapters change a token's results, Inf and NaN included.
+ * In fp16, |s_a U| and |dU| have to stay below 65504, as activations do.
  * Other arguments as qlora_linear_fwd (adapter_idx and scales need 4-byte alignment).
  * Errors: QLORA_ERR_INVALID_ARG for n_adapters outside 1 .. 65535, QLORA_ERR_SHAPE
  * when n_adapters * N is above 2^31 - 513, and those of qlora_linear_fwd.
