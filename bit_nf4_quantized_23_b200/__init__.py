@@ -348,9 +348,14 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
+# The calls below are short next to a Python function call, so their checks read each attribute once and
+# hand ctypes plain integers.
+_DTYPE_CODES = {torch.bfloat16: QLORA_DTYPE_BF16, torch.float16: QLORA_DTYPE_F16, torch.float32: QLORA_DTYPE_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream without a Stream object
+
+
 def _need_on(t: torch.Tensor, dtype, name: str, shape, dev: int) -> int:
-    """_need, and on CUDA device `dev`, the current one, where the library launches; returns the address.
-    One pass over the attributes when all is well: these checks are a part of a small call's time."""
+    """_need, and on CUDA device `dev`, the current one, where the library launches; returns the address."""
     try:
         if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
             return t.data_ptr()
@@ -371,7 +376,9 @@ def _device_of(t: torch.Tensor, name: str) -> int:
 
 
 def _stream_on(stream, dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 @lru_cache(maxsize=256)
@@ -454,11 +461,15 @@ def _rows(t: torch.Tensor, name: str, dev: int, shape=None):
     code, row stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    code = _dtype_code(t.dtype)
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16, torch.float16 or torch.float32, got {t.dtype}")
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}, "
-                         f"got {tuple(t.shape)}")
-    (M, V), (ld, one) = t.shape, t.stride()
+                         f"got {tuple(size)}")
+    M, V = size
+    ld, one = t.stride()
     if M <= 1:
         ld = max(V, 1)
     if t.get_device() != dev or (V > 1 and one != 1) or ld < V:
@@ -470,10 +481,13 @@ def _topk_args(logits, teacher_idx, teacher_logits, dev):
     z_code, ld = _rows(logits, "logits", dev)
     if not isinstance(teacher_idx, torch.Tensor) or teacher_idx.dim() != 2:
         raise ValueError("teacher_idx must be a 2-D tensor [M, k]")
-    shape = (logits.shape[0], teacher_idx.shape[1])
-    t_code = _dtype_code(teacher_logits.dtype)
-    return (z_code, ld, shape[1], t_code, _need_on(teacher_idx, torch.int32, "teacher_idx", shape, dev),
-            _need_on(teacher_logits, teacher_logits.dtype, "teacher_logits", shape, dev))
+    k = teacher_idx.shape[1]
+    shape, t_dtype = (logits.shape[0], k), teacher_logits.dtype
+    t_code = _DTYPE_CODES.get(t_dtype)
+    if t_code is None:
+        raise TypeError(f"teacher_logits must be torch.bfloat16, torch.float16 or torch.float32, got {t_dtype}")
+    return (z_code, ld, k, t_code, _need_on(teacher_idx, torch.int32, "teacher_idx", shape, dev),
+            _need_on(teacher_logits, t_dtype, "teacher_logits", shape, dev))
 
 
 def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,

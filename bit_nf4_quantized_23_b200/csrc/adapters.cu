@@ -444,10 +444,10 @@ finish_part(FinishSource s0, FinishSource s1, int64_t M, int r, int Rn, int R, i
 // of N = RB for each part when that exceeds 256); the epilogue adds the parts in fp32.
 // Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 zero the rows of other
 // tokens in tiles that the adapter shares, then run the epilogue.
-// Every 32 token tiles the accumulators are added to the output and begun anew: the tensor cores' fp32
+// Every 16 token tiles the accumulators are added to the output and begun anew: the tensor cores' fp32
 // sums lose about 2^-27 of themselves at each 16-wide step, one way, which a long batch would notice.
 constexpr int kGradThreads = 192;
-constexpr int kGradFlush = 32;
+constexpr int kGradFlush = 16;
 
 struct GradParams {
     int64_t M, K, N;
@@ -723,12 +723,12 @@ struct AdaptersWs {
 
 // Splits of the reduction of U or dU: two CTAs for each of 148 SMs (a count fixed here, so that the
 // workspace does not depend on the current device) while each has at least two steps of 64, and no more
-// than 32 steps each: the tensor cores' fp32 sums lose about 2^-27 of themselves at every 16-wide step,
+// than 16 steps each: the tensor cores' fp32 sums lose about 2^-27 of themselves at every 16-wide step,
 // one way.  Rounded so that no split is empty.
 int part_splits(int64_t M, int64_t red, int32_t r) {
     const int64_t tiles = (M + kPartTile - 1) / kPartTile, steps = (red + 63) / 64;
     const int64_t most = r <= 128 ? 2 * 148 : 148;            // CTAs that run together
-    const int64_t want = std::max<int64_t>((steps + 31) / 32, std::min(most / tiles, steps / 2));
+    const int64_t want = std::max<int64_t>((steps + 15) / 16, std::min(most / tiles, steps / 2));
     const int64_t per = (steps + want - 1) / want;
     return (int)((steps + per - 1) / per);
 }
