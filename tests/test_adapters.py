@@ -430,6 +430,33 @@ def test_capture_and_replay_on_a_side_stream_with_new_inputs(M):
 
 
 @pytest.mark.gpu
+def test_two_calls_at_once_and_arguments_that_start_anywhere():
+    """Two streams with workspaces of their own, many calls in flight on each, against the same calls one
+    after the other; adapter_idx and scales start 4 bytes into their tensors."""
+    cases = [Case(90, 2048, 1024, 16, 7, "mixed", seed=11), Case(600, 1024, 2048, 32, 5, "runs", seed=12)]
+    for c in cases:
+        c.idx = torch.cat([c.idx[:1], c.idx])[1:]
+        c.scales = torch.cat([c.scales[:1], c.scales])[1:]
+        assert c.idx.data_ptr() % 16 == 4 and c.scales.data_ptr() % 16 == 4
+    want = []
+    for c in cases:
+        Y, U = c.fwd()
+        want.append((Y, U) + c.bwd(U_saved=U))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for i in range(6):
+        for k, c in enumerate(cases):
+            with torch.cuda.stream(streams[k]):
+                Y, U = c.fwd()
+                got[k].append((Y, U) + c.bwd(U_saved=U, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for run in got[k]:
+            for a, b in zip(want[k], run):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_need_dX_false_and_a_chain_through_the_distillation_loss():
     """An output projection with the adapters of three jobs, the loss of its logits against a teacher's
     top logits, and the backward through both; the gradients against the same chain in fp64 from the
