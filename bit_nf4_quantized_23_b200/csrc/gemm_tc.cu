@@ -457,6 +457,12 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
     const int hb = bn / 2;                                    // of which this CTA supplies
     raster_tile(blockIdx.x >> 1, (p.M + 511) / 512, (p.Nout + bn - 1) / bn, mt, nt);
     const int64_t m0 = mt * 512 + 256 * (int64_t)rank;       // this CTA's first token
+    // MULTI: accumulator h holds tokens 256 h + [0, 256) of the tile, 128 of them in each CTA, so that a tile
+    // of at most 256 tokens takes one accumulator and half of the MMAs (200 tokens, W[8192, 8192],
+    // the whole forward: 96 to 80 us)
+    const int halves = !MULTI || p.M - mt * 512 > 256 ? 2 : 1;
+    auto half_row = [&](int h) { return MULTI ? mt * 512 + 256 * h + 128 * (int64_t)rank : m0 + 128 * h; };
+    const uint32_t a_bytes = (uint32_t)halves * (kPairAStage / 2);   // token-tile bytes of this CTA and stage
     const int64_t n0 = nt * bn;                               // the pair's output column tile
     const int64_t nr0 = n0 + hb * (int64_t)rank;              // this CTA's output columns (forward: W rows)
     const uint32_t* const ad_list = MULTI ? p.ad.entry + mt * p.ad.cap * kAdEntry : nullptr;   // a pair's tile is kAdTile
@@ -514,8 +520,14 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
             if (ptx::elect_one_sync()) {
                 const uint32_t a_dst = sA + s * kPairAStage;
                 if (it < ks0) {
-                    if (leader) ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * kPairAStage);
-                    ptx::tma_load_2d_pair(a_dst, &tmA0, (kb0 + it) * 64, (int32_t)m0, lead_full_a + 8 * s);
+                    if (leader) ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * a_bytes);
+                    if (MULTI) {
+                        for (int h = 0; h < halves; ++h)
+                            ptx::tma_load_2d_pair(a_dst + h * 16384, &tmA0, (kb0 + it) * 64, (int32_t)half_row(h),
+                                                  lead_full_a + 8 * s);
+                    } else {
+                        ptx::tma_load_2d_pair(a_dst, &tmA0, it * 64, (int32_t)m0, lead_full_a + 8 * s);
+                    }
                     ptx::mbar_arrive_expect_tx(bar_codes + 8 * s, DX ? kPairCodesStage : 32u * (uint32_t)hb);
                     if (!DX)
                         ptx::tma_load_2d(sCodes + s * kPairCodesStage, &tmCodes, (kb0 + it) * 32, (int32_t)nr0,
@@ -529,9 +541,14 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                     // MULTI: the U2 tiles of the first adapter's steps serve the others'
                     const bool load_a = !MULTI || p.ksteps1 > kPairStages || it < ks0 + p.ksteps1;
                     if (leader)
-                        ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * ((load_a ? kPairAStage : 0u) +
+                        ptx::mbar_arrive_expect_tx(bar_full_a + 8 * s, 2 * ((load_a ? a_bytes : 0u) +
                                                                             (DX ? kPairBStage : 128u * (uint32_t)hb)));
-                    if (load_a) ptx::tma_load_2d_pair(a_dst, &tmA1, j * 64, (int32_t)m0, lead_full_a + 8 * s);
+                    if (MULTI) {
+                        for (int h = 0; h < halves && load_a; ++h)
+                            ptx::tma_load_2d_pair(a_dst + h * 16384, &tmA1, j * 64, (int32_t)half_row(h), lead_full_a + 8 * s);
+                    } else {
+                        ptx::tma_load_2d_pair(a_dst, &tmA1, j * 64, (int32_t)m0, lead_full_a + 8 * s);
+                    }
                     if (!DX) {
                         ptx::tma_load_2d_pair(sB + s * kPairBStage, &tmB1, jb * 64,
                                               (int32_t)nr0 + (MULTI ? adapter * p.ad.rows : 0), lead_full_a + 8 * s);
@@ -572,8 +589,7 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
             bool ok = true;
             int s = 0;
             uint32_t ph = 0;
-            // MULTI: lanes that the adapter at hand leaves alone (accumulator h: 128 tokens of each CTA
-            // of the pair), and the next adapter's 512, loaded ahead
+            // MULTI: lanes that the adapter at hand leaves alone, and the next adapter's 512, loaded ahead
             int je = -1;
             uint32_t off[2][8] = {}, off_next[16] = {};
             const uint32_t* ad_entry = ad_list;
@@ -582,7 +598,7 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                 if (MULTI && it >= ks0 && (it == ks0 || ++je == p.ksteps1)) {
                     je = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) off[(i >> 2) & 1][(i & 3) + 4 * (i >> 3)] = off_next[i];
+                    for (int i = 0; i < 16; ++i) off[i >> 3][i & 7] = off_next[i];
                     ad_entry += kAdEntry;
                     if (it + p.ksteps1 < ktotal) load_lanes_off<16>(ad_entry, off_next);
                 }
@@ -608,6 +624,10 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
                                                                 bdesc, idesc, 1u, o);
                             }
                         }
+                    } else if (MULTI && halves == 1) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16_ss_pair(tmem, ad + kk * (32 >> 4), bd + kk * kstep, idesc, (it | kk) != 0 ? 1u : 0u);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -713,8 +733,8 @@ tc_gemm_nf4_pair(const __grid_constant__ CUtensorMap tmA0, const __grid_constant
             const uint32_t quad = (uint32_t)(warp & 3);
             const int half = (warp - 2) >> 2;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int64_t m = m0 + h * 128 + quad * 32 + lane;
+            for (int h = 0; h < halves; ++h) {
+                const int64_t m = half_row(h) + quad * 32 + lane;
 #pragma unroll 1
                 for (int cc = 0; cc < kBN / 64; ++cc) {
                     const int c = half * (kBN / 64) + cc;
@@ -1359,45 +1379,40 @@ static int pair_tile_width(int64_t M, int64_t N) {
     return best;
 }
 
-// The same choice for the forward with one adapter per token, whose batches are often below one wave: a
-// K-step of a pair tile takes about 66 + its width (in units of a column's share; measured at 400 tokens,
-// W[4096, 4096]: 49, 44, 39 and 34 us at 256, 224, 192 and 160 columns; odd multiples of 16 are slower).
-static int adapters_tile_width(int64_t M, int64_t N) {
-    const int64_t mtiles = (M + 511) / 512;
-    int best = kBN;
-    int64_t best_cost = INT64_MAX;
+// One adapter per token: whether a product runs on CTA pairs, the columns of a pair's tile (forward; dX has
+// kBN) and the splits of the reduction over the frozen weight, chosen together, since these batches are often
+// below one wave.  By the time of each choice: a K-step of a pair takes 2.4 ns times 66 + its width (400
+// tokens, W[4096, 4096], 64 steps: 49, 44, 39 and 34 us at 256, 224, 192 and 160 columns; odd multiples of
+// 16 are slower) and a single CTA's, for up to 256 tokens, 1 us (200 tokens, W[8192, 8192], 128 steps:
+// 127 us).  Splits, of at least 16 steps each and one wave in all, cost the sum over their fp32 partial
+// outputs: 3 us, and 8 bytes an element and split at 5 TB/s (200 tokens, W[8192, 8192], the whole forward:
+// 80 us in one piece, 61 us as two halves of wider tiles; with 8 steps a split W[1024, 1024] loses 1 to 3 us).
+struct AdaptersPlan {
+    bool pairs;
+    int bn, splits;
+};
+
+static AdaptersPlan adapters_plan(int64_t M, int64_t Nout, int64_t red, bool dx) {
+    const int64_t steps = (red + 63) / 64;
+    AdaptersPlan best = {false, kBN, 1};
+    double best_ns = M > 256 ? 1e300 : 1000.0 * (double)(((Nout + kBN - 1) / kBN + 147) / 148 * steps);
     for (int bn : {256, 224, 192, 160}) {
-        const int64_t cost = (mtiles * ((N + bn - 1) / bn) + 73) / 74 * (66 + bn);
-        if (cost < best_cost) { best_cost = cost; best = bn; }
+        const int64_t pairs = (M + 511) / 512 * ((Nout + bn - 1) / bn);
+        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(74 / pairs, steps / 16));
+        for (int64_t want = 1; want <= most; ++want) {
+            const int64_t per = (steps + want - 1) / want, splits = (steps + per - 1) / per;
+            const double ns = 2.4 * (66 + bn) * (double)((pairs * splits + 73) / 74 * per) +
+                              (splits > 1 ? 3000.0 + 0.0016 * (double)(M * Nout * splits) : 0.0);
+            if (ns < best_ns) { best_ns = ns; best = {true, bn, (int)splits}; }
+        }
+        if (dx) break;
     }
     return best;
 }
 
-// One adapter per token: also up to 256 tokens on CTA pairs unless the single CTAs' tiles of 256
-// columns need so many fewer waves that they end first.  A K-step of a pair takes about two thirds of a
-// single CTA's (200 tokens, K = 8192: 96 against 127 us at N = 8192, one wave each; 185 against 132 us
-// at N = 28672, two waves of pairs).
-static bool use_pairs_adapters(int64_t M, int64_t Nout, int bn) {
-    if (M > 256) return true;
-    const int64_t pair_waves = ((Nout + bn - 1) / bn + 73) / 74, waves = ((Nout + kBN - 1) / kBN + 147) / 148;
-    return 2 * pair_waves <= 3 * waves;
-}
-
-// Splits of the reduction over the frozen weight, for batches whose pair tiles leave half of the GPU
-// idle: as many as fit on it, of at least 16 steps each, so that what a split saves (0.6 us a step)
-// outweighs the sum over the fp32 partial outputs.
-static int adapters_splits(int64_t M, int64_t Nout, int64_t red, int bn) {
-    const int64_t pairs = (M + 511) / 512 * ((Nout + bn - 1) / bn), steps = (red + 63) / 64;
-    const int64_t want = std::min<int64_t>(74 / pairs, steps / 16);
-    if (want < 2) return 1;
-    const int64_t per = (steps + want - 1) / want;
-    return (int)((steps + per - 1) / per);
-}
-
 size_t adapters_split_bytes(int64_t M, int64_t N, int64_t K, bool dx) {
     const int64_t Nout = dx ? K : N;
-    const int bn = dx ? kBN : adapters_tile_width(M, N);
-    const int splits = use_pairs_adapters(M, Nout, bn) ? adapters_splits(M, Nout, dx ? N : K, bn) : 1;
+    const int splits = adapters_plan(M, Nout, dx ? N : K, dx).splits;
     return splits > 1 ? (size_t)splits * ((size_t)(M * Nout + 3) / 4 * 4) * sizeof(float) : 0;
 }
 
@@ -1499,10 +1514,11 @@ qlora_status launch_tc_decode(const DecodeArgs& a, cudaStream_t stream) {
 qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     const qlora_nf4_weight* w = a.w;
     const int64_t N = w->N, K = w->K;
-    const bool pair = a.n_adapters > 0 ? use_pairs_adapters(a.p.M, dx ? K : N, dx ? kBN : adapters_tile_width(a.p.M, N))
-                                       : use_pairs(a.p.M);
-    const uint32_t bm = pair || a.p.M > 128 ? 256 : 128;     // token rows of one copy: a pair CTA's, or the tile's
-    a.p.bn = !pair || dx ? kBN : a.n_adapters > 0 ? adapters_tile_width(a.p.M, N) : pair_tile_width(a.p.M, N);
+    const AdaptersPlan plan = a.n_adapters > 0 ? adapters_plan(a.p.M, dx ? K : N, dx ? N : K, dx) : AdaptersPlan{};
+    const bool pair = a.n_adapters > 0 ? plan.pairs : use_pairs(a.p.M);
+    // token rows of one copy: a pair CTA's (with adapters, one accumulator's 128 of them), or the tile's
+    const uint32_t bm = pair ? (a.n_adapters > 0 ? 128 : 256) : a.p.M > 128 ? 256 : 128;
+    a.p.bn = a.n_adapters > 0 ? plan.bn : !pair || dx ? kBN : pair_tile_width(a.p.M, N);
     const uint32_t wrows = pair ? (uint32_t)a.p.bn / 2 : 256;   // forward: W rows one CTA loads codes (and LoRA B rows) for
     // segment 0: A (X or dY) and the packed codes
     if (!dx) {
@@ -1557,7 +1573,7 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
     if (!a.p.err) return QLORA_ERR_CUDA;
     if (a.n_adapters > 0) {
         if (pair) {
-            const int splits = a.split_out ? adapters_splits(a.p.M, a.p.Nout, dx ? N : K, a.p.bn) : 1;
+            const int splits = a.split_out ? plan.splits : 1;
             a.p.split_steps = (a.p.ksteps0 + splits - 1) / splits;
             void* out = a.p.out;
             const bool out_f32 = a.p.out_f32 != 0;
