@@ -229,6 +229,15 @@ def test_few_tiles_and_a_long_reduction(M, N, K, r, n, dt, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n", [(129, 4100, 2048, 16, 5), (255, 1500, 1088, 40, 6), (640, 300, 2176, 20, 9), (768, 1050, 192, 64, 4),
+                                       (769, 200, 1088, 33, 5), (1280, 72, 64, 100, 3)])
+@pytest.mark.parametrize("rows", ["runs", "mixed"])
+def test_tiles_that_end_at_or_beside_half_of_their_tokens(M, N, K, r, n, rows):
+    """Tiles of 512 tokens of which the last has at most 256, or a few more, whole and split reductions."""
+    check(Case(M, N, K, r, n, rows, seed=6))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,r,n,dt", [(112, 28672, 8192, 64, 6, F16), (48, 8192, 8192, 16, 32, BF16), (4, 11008, 4096, 16, 4, BF16),
                                           (700, 8192, 4096, 32, 9, BF16), (200, 4096, 11008, 64, 3, F16)])
 def test_full_size_layers_repeat_bit_for_bit(M, N, K, r, n, dt):
