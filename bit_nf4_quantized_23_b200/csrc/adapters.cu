@@ -712,8 +712,9 @@ inline int32_t grad_ranks(int32_t r) { return (int32_t)round_up(r, grad_block(r)
 
 // Workspace, every piece 256-byte aligned:
 //   the lists; V2, 16-bit [M, 2R] (hi | lo of s U in the forward, of dU in the backward); U3 and dU3,
-//   16-bit [M, 3 Rg] (three parts of s U and of dU); split, fp32 partial outputs of a split reduction; partial fp32 (splits of U or dU, or the small-M forward's partial tiles); B8, B_all with
-//   its rows padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
+//   16-bit [M, 3 Rg] (three parts of s U and of dU); partial, fp32 (splits of U or dU, or the small-M
+//   forward's partial tiles); split, fp32 partial outputs of a split reduction; B8, B_all with its rows
+//   padded to 16 bytes (r % 8 != 0); dY8 likewise (N % 8 != 0).
 struct AdaptersWs {
     size_t tok, n512, e512, n_grad, e_grad, v2, u3, du3, part, split, b8, dy8, total;
     size_t split_bytes;
@@ -865,8 +866,8 @@ qlora_status launch_grads(const void* X, const void* dY, int64_t ldy, int64_t M,
     p.v_bytes = (uint32_t)((3 * RB + 63) / 64) * 8192u;
     p.tmem_cols = RB <= 32 ? 128u : RB <= 64 ? 256u : 512u;
     // as many stages as fit in half of the shared memory (two CTAs per SM), else one CTA's worth
-    uint32_t stages = (kMaxSmem / 2 - 3072) / (kStage16K + p.v_bytes);
-    if (stages < 2) stages = (kMaxSmem - 3072) / (kStage16K + p.v_bytes);
+    uint32_t stages = (kMaxSmem / 2 - 3 * 1024) / (kStage16K + p.v_bytes);
+    if (stages < 2) stages = (kMaxSmem - 3 * 1024) / (kStage16K + p.v_bytes);
     p.stages = std::min(stages, 4u);
     p.f16 = f16;
     p.n_grad = l.n_grad; p.e_grad = l.e_grad; p.tiles64 = l.tiles64;

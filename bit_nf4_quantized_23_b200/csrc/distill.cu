@@ -7,7 +7,9 @@
 //     lse   = log sum_v exp(z_v/T)                            (over the whole vocabulary)
 //     loss  = T^2 sum_j p_j (log p_j - (z_{i_j}/T - lse))     (KL divergence, scaled by T^2)
 //     dz_v  = dloss T (exp(z_v/T - lse) - sum_{j: i_j = v} p_j)
-// A row without valid entries (none given, or every t_j = -inf) has loss 0 and gradient 0.
+// A row without valid entries (none given, or every t_j = -inf) has loss 0 and gradient 0, and so has a row
+// whose logits are all masked, by -inf or by a type's lowest value (lse below -6e29, far from any logit of
+// a model, where one fp32 number cannot hold both the mask and log V): its lse is -inf.
 //
 // Both kernels are bound by HBM: the forward reads every logit once (running maximum and sum of
 // the softmax in registers, fp32, base-2 exponentials), the backward reads and writes every
@@ -292,9 +294,10 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const bool masked = lse2 < -1e30f;                        // false for NaN
     if (threadIdx.x == 0) {
-        p.lse[m] = lse2 * kLn2;
-        p.loss[m] = teacher.some ? p.T2 * kLn2 * sum : 0.f;
+        p.lse[m] = masked ? -INFINITY : lse2 * kLn2;
+        p.loss[m] = teacher.some && !masked ? p.T2 * kLn2 * sum : 0.f;
     }
 }
 
@@ -323,10 +326,10 @@ distill_bwd(DistillParams p) {
     // Only what the dense pass must wait for comes before it: whether the row has an entry, and the
     // entries' logits of this part, which it may overwrite (the gradient may take the logits' place).  The
     // teacher's softmax follows the pass.
-    const float g = p.dloss[m], scale = g * p.T, l2 = __fmul_rn(p.lse[m], (float)kLog2e);
+    const float g = p.dloss[m], scale = g * p.T, lse = p.lse[m], l2 = __fmul_rn(lse, (float)kLog2e);
     float z[kTopPerThread];
     const bool entry = load_entries<DT_IN>(p, m, row, lo, hi, last ? head : 0, entries, z);
-    const bool zero = !__syncthreads_or(entry) || g == 0.f;
+    const bool zero = !__syncthreads_or(entry) || g == 0.f || lse == -INFINITY;
 
     if (VEC) {
         // measured best of 2 to 8 loads per thread, and of 3 to 8 blocks per SM

@@ -385,9 +385,11 @@ qlora_status qlora_dequantize_int8_absmax(const int8_t* codes, const float* alph
  *     lse  = log sum_v exp(z_v / T) over the whole row,
  *     loss = T^2 sum_j p_j (log p_j - z_{i_j} / T + lse).
  * An index that comes twice is two entries of the same logit.  A row without
- * entries, or whose teacher logits are all -inf, has loss 0.
+ * entries, or whose teacher logits are all -inf, has loss 0.  So has a row whose
+ * own logits are all masked, by -inf or a type's lowest value: lse is -inf there.
  *   logits          device [M, V] of z_dtype (any qlora_dtype), rows ld >= V elements
- *                   apart; every row holds a finite logit.  -inf logits have probability 0.
+ *                   apart.  -inf logits have probability 0.  The fp32 lse limits what large
+ *                   logits keep: q_v is good to 2^-23 |lse| of itself.
  *   teacher_idx     device int32 [M, k];  1 <= k <= 1024.
  *   teacher_logits  device [M, k] of t_dtype (any qlora_dtype).
  *   temperature     1e-3 .. 1e3.
@@ -405,7 +407,8 @@ qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t
 /*
  * Gradient of sum_m dloss[m] loss[m] with respect to the logits:
  *     dz_v = dloss T (exp(z_v / T - lse) - sum_{j: i_j = v} p_j),  rounded once to d_dtype,
- * and zeros in a row without entries or with dloss[m] = 0 (its logits are not read).
+ * and zeros in a row without entries, with dloss[m] = 0 or with lse[m] = -inf
+ * (its logits are not used).
  *   lse       device fp32 [M] from the forward with the same arguments.
  *   dloss     device fp32 [M].
  *   dlogits   device [M, V] of d_dtype (any qlora_dtype), rows ldd >= V elements apart;

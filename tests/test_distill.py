@@ -253,6 +253,32 @@ def test_rows_without_entries_masks_and_repeated_indices(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [0.5, 1.0, 30.0])
+@pytest.mark.parametrize("M,V", [(5, 9), (5, 30011), (700, 515)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_rows_whose_own_logits_are_all_masked(M, V, T, dt):
+    """Such a row has loss 0, gradient 0 and lse -inf; rows beside it, and a row with one logit left, do not."""
+    z, idx, t, dloss = make(M, V, 4, dt, torch.float32, seed=3)
+    idx[:, 0] = 1
+    plain = check_case(z, idx, t, T, dloss, dt)
+    z = z.clone()
+    z[0] = -math.inf
+    z[1] = torch.finfo(dt).min
+    z[2, ::2], z[2, 1::2] = -math.inf, torch.finfo(dt).min
+    z[3] = torch.finfo(dt).min
+    z[3, 1], idx[3, 1:] = 2.5, -1                                # the teacher's one choice is the one logit left
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, T)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, T)
+    assert torch.all(lse[:3] == -math.inf) and torch.all(loss[:3] == 0) and torch.all(dz[:3] == 0)
+    # q = p = 1: lse is 2.5 / T to four roundings of a value below 8 / T, and all else follows from it
+    e = 2.0 ** -22 * 8 / T
+    assert abs(float(lse[3]) - 2.5 / T) <= e and abs(float(loss[3])) <= 2 * T * T * e
+    assert torch.all(dz[3].float().abs() <= 2 * T * e * dloss[3])
+    for new, old in zip((loss, lse, dz), plain):
+        assert torch.equal(new[4:], old[4:])
+
+
+@pytest.mark.gpu
 def test_a_teacher_index_behind_the_vocabulary_is_flagged_and_skipped():
     z, idx, t, dloss = make(3, 500, 4, torch.bfloat16, torch.float32, seed=9)
     q4.qlora_read_device_errors(clear=True)
