@@ -381,9 +381,12 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
                     ptx::tmem_ld_32x32b_x32(tmem + ((quad * 32u) << 16) + 256u * (uint32_t)g + c, v);
                     ptx::tmem_ld_wait();
                     if (c < hi && c + 32 > lo) {
-                        uint4* d4 = reinterpret_cast<uint4*>(dst + c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) d4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        for (int i = 0; i < 32; i += 8)       // whole 32-byte sectors: 29.6 to 26 us at 100 tokens, W[1024, 1024]
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + i),
+                                         "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]),
+                                         "r"(v[i + 6]), "r"(v[i + 7])
+                                         : "memory");
                     }
                 }
             }
@@ -526,19 +529,27 @@ rows_finish_U(FixParams p) {
 // output type.  CTA x: columns 64 x .. 64 x + 63 of every token (128 accumulator rows).  The adapter term
 // is the fused GEMM's: hi and lo of s_a U meet the adapter's B on the tensor cores, and the MMAs of one
 // adapter write only its tokens' rows.  The four epilogue warps sum the base product meanwhile.
-// Roles (192 threads): warp 0 TMA, warp 1 TMEM owner + MMA issuer, warps 2-5 one thread per token.
+//
+// The kernel starts when every CTA of rows_finish_U has seen the rows kernel complete (it lets dependents
+// start after its own wait), so only U2 has to be waited for: the partial tiles, the tokens' places and B
+// are read at once (48 tokens, W[8192, 8192], the whole forward: 50.7 to 49.5 us).  Such reads pass by L1
+// (__ldcg, TMA), which may hold lines of an earlier call.
+// Roles (192 threads): warp 0 TMA of B, warp 1 TMEM owner, U2 + MMA issuer, warps 2-5 one thread per token.
 constexpr int kFixThreads = 192;
 constexpr uint32_t kFixB = 64 * 128;              // B stage: 64 columns of the output x 64 ranks
 constexpr int kFixStages = 4;
 constexpr uint32_t kFixU = 128 * 128;             // one 64-wide image of U2
 
+constexpr uint32_t kFixSumRow = (64 + 4) * 4;     // a token's sums, padded so that 8 rows' 16 bytes meet no bank twice
+
 struct FixLayout {
-    uint32_t off_b, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
+    uint32_t off_b, off_sum, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
 };
-__host__ __device__ inline FixLayout fix_layout(uint32_t images) {
+__host__ __device__ inline FixLayout fix_layout(uint32_t images, uint32_t tokens) {
     FixLayout l;
     l.off_b = images * kFixU;
-    l.off_mask = l.off_b + kFixStages * kFixB;
+    l.off_sum = l.off_b + kFixStages * kFixB;
+    l.off_mask = l.off_sum + tokens * kFixSumRow;
     l.off_adapter = l.off_mask + 128 * 16;
     l.off_bars = l.off_adapter + 128 * 4;
     l.off_slot = l.off_bars + (2 * kFixStages + 2) * 8;
@@ -547,13 +558,51 @@ __host__ __device__ inline FixLayout fix_layout(uint32_t images) {
     return l;
 }
 
+// dst[m, 0 .. 64) = the sum of src[b, m, 0 .. 64) over the slots b < n, in order: I chunks of four columns
+// a thread and B slots of each in flight.  For a few tokens that spreads a tile's many slots over threads
+// that had no token (4 tokens, W[4096, 4096], the whole forward: 21.6 to 20.5 us).
+template <int I, int B>
+__device__ __forceinline__ void sum_slots(const float* src, int64_t slot_floats, int n, int M, int t, char* dst) {
+    for (int i0 = t; i0 < M * 16; i0 += 128 * I) {
+        float4 acc[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = 0; b0 < n; b0 += B) {
+            float4 v[I][B];
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const int at = i0 + 128 * i;
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    v[i][b] = at < M * 16 && b0 + b < n
+                                  ? __ldcg(reinterpret_cast<const float4*>(src + (b0 + b) * slot_floats + (at >> 4) * 256) + (at & 15))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    acc[i].x = __fadd_rn(acc[i].x, v[i][b].x);
+                    acc[i].y = __fadd_rn(acc[i].y, v[i][b].y);
+                    acc[i].z = __fadd_rn(acc[i].z, v[i][b].z);
+                    acc[i].w = __fadd_rn(acc[i].w, v[i][b].w);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int at = i0 + 128 * i;
+            if (at < M * 16) reinterpret_cast<float4*>(dst + (at >> 4) * kFixSumRow)[at & 15] = acc[i];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kFixThreads)
 tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ CUtensorMap tmB, FixParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - ptx::smem_addr(smem_raw));
     const int images = 2 * p.R / 64;
-    const FixLayout lay = fix_layout((uint32_t)images);
+    const FixLayout lay = fix_layout((uint32_t)images, p.nt);
     const uint32_t sU = base, sB = base + lay.off_b;
     const uint32_t bar_full = base + lay.off_bars, bar_empty = bar_full + 8 * kFixStages;
     const uint32_t bar_u = bar_empty + 8 * kFixStages, bar_acc = bar_u + 8;
@@ -581,18 +630,17 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         ptx::tmem_alloc(base + lay.off_slot, 64);
         ptx::tmem_relinquish();
     }
-    grid_dependency_wait();                                   // partial tiles and U2 are complete
     allow_dependents();
     __syncthreads();
-    const int used = p.meta[0];
+    const int used = __ldcg(p.meta);
     int place = -1;
     if (warp >= 2) {                                          // one thread per token: the lanes of each adapter
-        const int m = tid - 64;
-        place = m < p.M ? p.meta[1 + m] : -1;
+        const int m = ((warp & 3) << 5) + lane;
+        place = m < p.M ? __ldcg(p.meta + 1 + m) : -1;
         const uint32_t same = __match_any_sync(0xffffffffu, place);
         if (place >= 0 && lane == __ffs((int)same) - 1) {
             mask[place * 4 + (m >> 5)] = ~same;
-            adapter[place] = p.idx[m];
+            adapter[place] = __ldcg(p.idx + m);
         }
     }
     ptx::tc_fence_before();
@@ -602,11 +650,6 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
     const int chunks = p.R >= 64 ? p.R / 64 : 1, steps = used * chunks;
 
     if (warp == 0) {
-        if (steps > 0 && ptx::elect_one_sync()) {
-            ptx::mbar_arrive_expect_tx(bar_u, (uint32_t)images * kFixU);
-            for (int c = 0; c < images; ++c) ptx::tma_load_2d(sU + c * kFixU, &tmU2, c * 64, 0, bar_u);
-        }
-        __syncwarp();
         int issued = 0, s = 0;
         uint32_t ph = 1;
         for (int i = 0; i < steps; ++i) {
@@ -622,7 +665,6 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
             if (++s == kFixStages) { s = 0; ph ^= 1u; }
         }
         if (*abort) {   // drain this CTA's copies in flight before it exits
-            if (steps > 0) ptx::mbar_wait_drain(bar_u, 0);
             for (int i = max(0, issued - kFixStages); i < issued; ++i)
                 ptx::mbar_wait_drain(bar_full + 8 * (i % kFixStages), (uint32_t)(i / kFixStages) & 1u);
         }
@@ -630,6 +672,12 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         const uint32_t idesc = ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, 64, 0, 0), p.f16 != 0);
         const uint64_t u_sw = ptx::smem_desc_sw128(sU, 16, 1024), b_sw = ptx::smem_desc_sw128(sB, 16, 1024);
         const bool packed = p.R == 32;                        // hi and lo halves of 32 ranks in one image
+        grid_dependency_wait();                               // U2 is complete
+        if (steps > 0 && ptx::elect_one_sync()) {
+            ptx::mbar_arrive_expect_tx(bar_u, (uint32_t)images * kFixU);
+            for (int c = 0; c < images; ++c) ptx::tma_load_2d(sU + c * kFixU, &tmU2, c * 64, 0, bar_u);
+        }
+        __syncwarp();
         bool ok = steps == 0 || __all_sync(0xffffffffu, ptx::mbar_wait(bar_u, 0, abort, p.err));
         int s = 0;
         uint32_t ph = 0;
@@ -656,7 +704,10 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         }
         if (ptx::elect_one_sync()) {
             ptx::mma_commit(bar_acc);
-            if (*abort) ptx::mbar_wait_drain(bar_acc, 0);   // issued MMAs finish before TMEM is freed
+            if (*abort) {   // its copies and issued MMAs finish before the CTA exits and TMEM is freed
+                if (steps > 0) ptx::mbar_wait_drain(bar_u, 0);
+                ptx::mbar_wait_drain(bar_acc, 0);
+            }
         }
         __syncwarp();
     } else {
@@ -666,27 +717,14 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         const int tile = u_tiles + (int)(blockIdx.x >> 2);
         const int2 sp = unit_span((int64_t)tile * p.steps, p.steps, (int64_t)(u_tiles + p.w_tiles) * p.steps, p.G);
         const int slot0 = u_tiles * pieces_of(p.steps) + (tile - u_tiles) + sp.x;
-        const bool has = m < p.M && p.meta[1 + m] >= 0;
+        const bool has = place >= 0;
         const int64_t slot_floats = (int64_t)p.nt * 256;
         const bool live = (int)(quad * 32u) < p.M;
-        float acc[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-        if (m < p.M) {
-            const float* src = p.partial + (int64_t)slot0 * slot_floats + (int64_t)m * 256 + col0;
-            for (int b = sp.x; b <= sp.y; ++b, src += slot_floats) {
-                float4 v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = reinterpret_cast<const float4*>(src)[i];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    acc[4 * i] = __fadd_rn(acc[4 * i], v[i].x);
-                    acc[4 * i + 1] = __fadd_rn(acc[4 * i + 1], v[i].y);
-                    acc[4 * i + 2] = __fadd_rn(acc[4 * i + 2], v[i].z);
-                    acc[4 * i + 3] = __fadd_rn(acc[4 * i + 3], v[i].w);
-                }
-            }
-        }
+        const float* src = p.partial + (int64_t)slot0 * slot_floats + col0;
+        char* sums = reinterpret_cast<char*>(gbase + lay.off_sum);
+        if (p.M <= 8) sum_slots<1, 12>(src, slot_floats, sp.y - sp.x + 1, p.M, tid - 64, sums);
+        else sum_slots<4, 4>(src, slot_floats, sp.y - sp.x + 1, p.M, tid - 64, sums);
+        asm volatile("bar.sync 1, 128;" ::: "memory");        // the sums of other threads
         const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
         ptx::tc_fence_after();
         if (acc_ok && live) {
@@ -697,8 +735,14 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
                 ptx::tmem_ld_32x32b_x32(tmem + ((quad * 32u) << 16) + c * 32, v);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = __float_as_uint(has ? __fadd_rn(acc[32 * c + i], __uint_as_float(v[i])) : acc[32 * c + i]);
+                for (int i = 0; i < 8; ++i) {
+                    if (m >= p.M) break;
+                    const float4 y = reinterpret_cast<const float4*>(sums + m * kFixSumRow)[8 * c + i];
+                    const float x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[4 * i + e] = __float_as_uint(has ? __fadd_rn(x[e], __uint_as_float(v[4 * i + e])) : x[e]);
+                }
                 if (m < p.M) store_row32(p.out, p.out_f32 != 0, p.f16 != 0, p.N, m, n0 + 32 * c, p.N, v);
             }
         }
@@ -789,7 +833,7 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (!make_tmap_2d(&tmU2, true, a.U2, 2 * a.R, a.M, 4 * a.R, 64, 128, true)) return QLORA_ERR_CUDA;
     if (!make_tmap_2d(&tmB, true, a.B, a.ldb, (uint64_t)a.n_adapters * N, a.ldb * 2, 64, 64, true)) return QLORA_ERR_CUDA;
     (void)launch_dependent(tc_rows_fixup, dim3((unsigned)((N + 63) / 64)), dim3(kFixThreads),
-                           fix_layout((uint32_t)(2 * a.R / 64)).alloc, stream, tmU2, tmB, f);
+                           fix_layout((uint32_t)(2 * a.R / 64), f.nt).alloc, stream, tmU2, tmB, f);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
