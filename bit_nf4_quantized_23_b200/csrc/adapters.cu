@@ -349,10 +349,10 @@ tc_part_gemm(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CU
                 ptx::tmem_ld_32x32b_x16(tmem + ((quad * 32u) << 16) + c * 16, v);
                 ptx::tmem_ld_wait();
                 if (row < p.M) {
-                    uint4* d4 = reinterpret_cast<uint4*>(dst + c * 16);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d4[i] = have ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 16; ++i) v[i] = have ? v[i] : 0u;
+                    store_sector(dst + c * 16, v);
+                    store_sector(dst + c * 16 + 8, v + 8);
                 }
             }
         }
@@ -592,6 +592,7 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
         float* const dst = is_a ? p.dA + ((int64_t)ad * p.r + j0) * p.K + orow : p.dB + ((int64_t)ad * p.N + orow) * p.r + j0;
         const int64_t pitch = is_a ? p.K : 1;                 // between a thread's ranks
         const bool vec = !is_a && p.r % 4 == 0;
+        const bool sectors = !is_a && p.r % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dB) & 31u) == 0;
         const float down = p.f16 ? 1.f / kPartScale : 1.f;
         // the accumulators of piece f of the token tiles, stored (f = 0) or added to what the thread stored
         auto flush = [&](int f) -> bool {
@@ -621,7 +622,13 @@ tc_adapter_grads(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         if (c * 16 + q < nj) v[q] = __fadd_rn(at[q * pitch], v[q]);
-                if (vec) {
+                if (sectors) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(v[q]);
+                    store_sector(at, w);
+                    if (c * 16 + 8 < nj) store_sector(at + 8, w + 8);
+                } else if (vec) {
 #pragma unroll
                     for (int q = 0; q < 16; q += 4)
                         if (c * 16 + q < nj) *reinterpret_cast<float4*>(at + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);

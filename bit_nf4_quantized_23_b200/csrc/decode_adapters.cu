@@ -383,10 +383,7 @@ tc_rows_nf4(const __grid_constant__ CUtensorMap tmCodes, const __grid_constant__
                     if (c < hi && c + 32 > lo) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)       // whole 32-byte sectors: 29.6 to 26 us at 100 tokens, W[1024, 1024]
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + i),
-                                         "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]),
-                                         "r"(v[i + 6]), "r"(v[i + 7])
-                                         : "memory");
+                            store_sector(dst + c + i, v + i);
                     }
                 }
             }

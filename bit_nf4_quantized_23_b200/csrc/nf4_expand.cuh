@@ -109,7 +109,10 @@ __device__ __forceinline__ void store_row32(void* out, bool out_f32, bool h, int
     const bool full = (nb + 32 <= nlim);
     if (out_f32) {
         float* dst = static_cast<float*>(out) + m * ldo + nb;
-        if (full && (ldo & 3) == 0) {
+        if (full && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_sector(dst + 8 * i, v + 8 * i);
+        } else if (full && (ldo & 3) == 0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 reinterpret_cast<uint4*>(dst)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -121,14 +124,16 @@ __device__ __forceinline__ void store_row32(void* out, bool out_f32, bool h, int
     } else {
         uint16_t* dst = static_cast<uint16_t*>(out) + m * ldo + nb;
         if (full && (ldo & 7) == 0) {
+            uint32_t o[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 o;
-                o.x = pack16x2_rn(__uint_as_float(v[8 * i + 0]), __uint_as_float(v[8 * i + 1]), h);
-                o.y = pack16x2_rn(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]), h);
-                o.z = pack16x2_rn(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]), h);
-                o.w = pack16x2_rn(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]), h);
-                reinterpret_cast<uint4*>(dst)[i] = o;
+            for (int i = 0; i < 16; ++i) o[i] = pack16x2_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), h);
+            if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+                store_sector(dst, o);
+                store_sector(dst + 16, o + 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         } else {
 #pragma unroll

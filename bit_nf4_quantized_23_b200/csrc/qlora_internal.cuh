@@ -104,6 +104,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// 32 bytes, 32-byte aligned, in one access: a thread that writes a row of its own then fills whole sectors.
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // The 16-bit compute types: bf16 (the default) or IEEE fp16, chosen per weight
 // (a warp-uniform flag in the kernels).  Round to nearest even in both.
 __device__ __forceinline__ uint32_t f32_to_f16_bits_rn(float x) {
