@@ -764,7 +764,7 @@ AdaptersWs adapters_ws(int64_t M, int64_t N, int64_t K, int32_t r, int64_t n) {
     w.split = piece(w.split_bytes);
     w.b8 = piece(r % 8 ? (size_t)n * N * round_up(r, 8) * 2 : 0);
     w.dy8 = piece(N % 8 ? (size_t)M * round_up(N, 8) * 2 : 0);
-    w.total = o;
+    w.total = o + 256;                                        // the caller's pointer is brought to 256 bytes
     return w;
 }
 
@@ -952,7 +952,7 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight* w, const void* X,
     if (!workspace || workspace_bytes < lw.total) return QLORA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    char* ws = static_cast<char*>(workspace);
+    char* ws = reinterpret_cast<char*>(align_up(reinterpret_cast<size_t>(workspace), 256));
     float* partial = reinterpret_cast<float*>(ws + lw.part);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
     void* U2 = ws + lw.v2;
@@ -1009,7 +1009,7 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight* w, const void* X,
     if (!workspace || workspace_bytes < lw.total) return QLORA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    char* ws = static_cast<char*>(workspace);
+    char* ws = reinterpret_cast<char*>(align_up(reinterpret_cast<size_t>(workspace), 256));
     float* partial = reinterpret_cast<float*>(ws + lw.part);
     const bool f16 = w->compute_dtype == QLORA_DTYPE_F16;
     const AdapterLists l = lists_at(ws, lw);

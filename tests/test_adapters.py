@@ -7,6 +7,7 @@ it in bf16, and by 2^-22 of it plus half of the smallest subnormal, 2^-25, in fp
 16-bit type add half a step.
 """
 import ctypes
+import math
 
 import pytest
 import torch
@@ -463,6 +464,34 @@ def test_two_calls_at_once_and_arguments_that_start_anywhere():
         for run in got[k]:
             for a, b in zip(want[k], run):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n", [(5, 264, 192, 16, 3), (60, 2048, 1024, 24, 5), (200, 512, 2048, 8, 4), (600, 256, 320, 32, 6)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_buffers_aligned_to_sixteen_bytes_only(M, N, K, r, n, out):
+    """Every buffer may start at any multiple of 16 bytes; the results are those of other starts, bit for bit."""
+    def shifted(shape, dtype):
+        size = math.prod(shape) * dtype.itemsize
+        raw = torch.full((size + 48,), 0xFF, dtype=torch.uint8, device="cuda")
+        at = 16 if raw.data_ptr() % 32 == 0 else 0
+        return raw[at:at + size].view(dtype).view(shape)
+
+    c = Case(M, N, K, r, n, "mixed", seed=15)
+    Y, U = c.fwd(y_dtype=out)
+    dX, dA, dB = c.bwd(U_saved=U, dx_dtype=out)
+    ws = shifted((q4.qlora_adapters_workspace_size(M, N, K, r, n),), torch.uint8)
+    Y2, U2 = c.fwd(y_dtype=out, out=shifted((M, N), out), U_out=shifted((M, r), F32), workspace=ws)
+    for name in ("X", "dY", "A", "B"):
+        v = getattr(c, name)
+        setattr(c, name, shifted(tuple(v.shape), v.dtype).copy_(v))
+    Y3, U3 = c.fwd(y_dtype=out, workspace=ws)
+    got = c.bwd(U_saved=U2, dx_dtype=out, dX=shifted((M, K), out), dA=shifted((n, r, K), F32), dB=shifted((n, N, r), F32),
+                workspace=ws)
+    assert all(t.data_ptr() % 32 == 16 for t in (ws, Y2, U2, c.X, c.dY, c.A, c.B) + got)
+    for a, b in zip((Y, U, Y, U, dX, dA, dB), (Y2, U2, Y3, U3) + got):
+        assert torch.equal(a, b)
+    assert q4.qlora_read_device_errors(clear=True) == 0
 
 
 @pytest.mark.gpu
