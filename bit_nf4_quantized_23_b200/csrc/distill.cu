@@ -59,16 +59,16 @@ __device__ __forceinline__ void store1(void* base, int64_t e, float v) {
     else static_cast<uint16_t*>(base)[e] = (uint16_t)to16_rn(v, DT == QLORA_DTYPE_F16);
 }
 
-// Eight consecutive elements as loaded (16 bytes of a 16-bit type, 32 of fp32); the address is
-// 16-byte aligned.
+// Eight consecutive elements as loaded, in one access that is aligned to its size (16 bytes of a 16-bit type,
+// 32 of fp32: a warp's two halves of 16 bytes would each touch every sector).
 template <int DT>
 struct Raw8 {
     uint4 a, b;
     __device__ __forceinline__ void load(const void* base, int64_t e) {
         if constexpr (DT == QLORA_DTYPE_F32) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e);
-            a = __ldcs(p);
-            b = __ldcs(p + 1);
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                         : "l"(static_cast<const float*>(base) + e));
         } else {
             a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e));
         }
@@ -98,9 +98,10 @@ struct Raw8 {
 template <int DT>
 __device__ __forceinline__ void store8(void* base, int64_t e, const float (&v)[8]) {
     if constexpr (DT == QLORA_DTYPE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e);
-        __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+        store_sector(static_cast<float*>(base) + e, w);
     } else {
         constexpr bool h = DT == QLORA_DTYPE_F16;
         __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e),
@@ -210,7 +211,7 @@ __device__ __forceinline__ float log2_p(const Teacher& t, float logit, float c) 
 }
 
 // Row layout of a part: elements [0, head) one by one, then chunks of eight from `head` on, then
-// the tail one by one; head brings the chunks to 16-byte boundaries.
+// the tail one by one; head brings the chunks to multiples of their size.
 template <int DT_IN>
 __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     grid_dependency_wait();
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     float z[kTopPerThread];
     if (part == 0) (void)load_entries<DT_IN>(p, m, row, 0, p.V, 0, entries, z);
 
-    const int64_t head = min(p.V, (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / kEs);
+    const int64_t head = min(p.V, (int64_t)(-(int64_t)(reinterpret_cast<uintptr_t>(row) / kEs) & 7));
     const int64_t chunks = (p.V - head) / 8;
     const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
     Softmax2 acc{-INFINITY, 0.f};
@@ -313,9 +314,8 @@ distill_bwd(DistillParams p) {
     constexpr int kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2, kEd = DT_OUT == QLORA_DTYPE_F32 ? 4 : 2;
     const char* row = static_cast<const char*>(p.logits) + m * p.ld * kEs;
     char* drow = static_cast<char*>(p.dlogits) + m * p.ldd * kEd;
-    // VEC: both rows are 16-byte aligned `head` elements in, as the narrower type's address says
-    const uintptr_t at = reinterpret_cast<uintptr_t>(kEd <= kEs ? drow : row);
-    const int64_t head = VEC ? min(p.V, (int64_t)(((16u - (uint32_t)(at & 15u)) & 15u) / (kEd <= kEs ? kEd : kEs))) : 0;
+    // VEC: chunks of eight are aligned to their size in both rows, from element `head` on
+    const int64_t head = VEC ? min(p.V, (int64_t)(-(int64_t)(reinterpret_cast<uintptr_t>(row) / kEs) & 7)) : 0;
     const int64_t chunks = VEC ? (p.V - head) / 8 : 0;
     const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
     const bool last = part == p.parts - 1;
@@ -333,7 +333,7 @@ distill_bwd(DistillParams p) {
 
     if (VEC) {
         // measured best of 2 to 8 loads per thread, and of 3 to 8 blocks per SM
-        constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : DT_OUT == QLORA_DTYPE_F32 ? 6 : 4;
+        constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : 4;
         int64_t c = c0 + threadIdx.x;
         if (zero) {
             const float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -431,13 +431,11 @@ cudaError_t run_fwd(const DistillParams& p, cudaStream_t s) {
 template <int DT_IN, int DT_OUT>
 cudaError_t run_bwd2(const DistillParams& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.M * p.parts));
-    // chunks of eight are 16-byte aligned in both rows when the rows' first elements lie alike modulo
-    // 16 bytes of the wider type
+    // chunks of eight are aligned in both rows when the rows' first elements lie alike modulo eight
     constexpr int64_t kEs = DT_IN == QLORA_DTYPE_F32 ? 4 : 2, kEd = DT_OUT == QLORA_DTYPE_F32 ? 4 : 2;
-    constexpr int64_t kPer16 = 16 / (kEs > kEd ? kEs : kEd);
-    const int64_t z0 = (int64_t)(reinterpret_cast<uintptr_t>(p.logits) & 15u) / kEs;
-    const int64_t d0 = (int64_t)(reinterpret_cast<uintptr_t>(p.dlogits) & 15u) / kEd;
-    if ((z0 - d0) % kPer16 == 0 && (p.ld - p.ldd) % kPer16 == 0)
+    const int64_t z0 = (int64_t)(reinterpret_cast<uintptr_t>(p.logits) / kEs & 7);
+    const int64_t d0 = (int64_t)(reinterpret_cast<uintptr_t>(p.dlogits) / kEd & 7);
+    if (z0 == d0 && (p.ld - p.ldd) % 8 == 0)
         return launch_dependent(distill_bwd<DT_IN, DT_OUT, true>, grid, dim3(kThreads), 0, s, p);
     return launch_dependent(distill_bwd<DT_IN, DT_OUT, false>, grid, dim3(kThreads), 0, s, p);
 }

@@ -415,8 +415,8 @@ qlora_status qlora_distill_topk_fwd(const void* logits, int32_t z_dtype, int64_t
  *             columns V .. ldd-1 are left as they are.  It may be the logits' own
  *             memory (same pointer, stride and element size); any other overlap is
  *             QLORA_ERR_INVALID_ARG.
- * Logits and gradient whose rows lie alike within 16 bytes (both contiguous, or both
- * with the same padding) take 16-byte accesses, others element by element.
+ * Logits and gradient whose rows start alike modulo eight elements (both contiguous,
+ * or both with the same padding) take wide accesses, others element by element.
  * Other arguments and errors as qlora_distill_topk_fwd.
  */
 qlora_status qlora_distill_topk_bwd(const void* logits, int32_t z_dtype, int64_t ld, int64_t M, int64_t V,
