@@ -473,7 +473,7 @@ struct FixParams {
     int32_t M, r, R, rp, steps, w_tiles, G;
     int32_t all_pieces;       // of A_all rows, at most
     uint32_t nt;
-    int32_t out_f32, f16;
+    int32_t out_f32, f16, stages;
     uint32_t* err;
 };
 
@@ -533,8 +533,10 @@ rows_finish_U(FixParams p) {
 // (__ldcg, TMA), which may hold lines of an earlier call.
 // Roles (192 threads): warp 0 TMA of B, warp 1 TMEM owner, U2 + MMA issuer, warps 2-5 one thread per token.
 constexpr int kFixThreads = 192;
+constexpr int kFixCtas = 4;                       // per SM, by their registers
+constexpr uint32_t kSmemPerSm = 228 * 1024;       // of which each CTA takes 1 KiB more than it asks for
 constexpr uint32_t kFixB = 64 * 128;              // B stage: 64 columns of the output x 64 ranks
-constexpr int kFixStages = 4;
+constexpr int kFixStages = 16;                    // of B, at most
 constexpr uint32_t kFixU = 128 * 128;             // one 64-wide image of U2
 
 constexpr uint32_t kFixSumRow = (64 + 4) * 4;     // a token's sums, padded so that 8 rows' 16 bytes meet no bank twice
@@ -542,10 +544,10 @@ constexpr uint32_t kFixSumRow = (64 + 4) * 4;     // a token's sums, padded so t
 struct FixLayout {
     uint32_t off_b, off_sum, off_mask, off_adapter, off_bars, off_slot, off_abort, alloc;
 };
-__host__ __device__ inline FixLayout fix_layout(uint32_t images, uint32_t tokens) {
+__host__ __device__ inline FixLayout fix_layout(uint32_t images, uint32_t tokens, uint32_t stages) {
     FixLayout l;
     l.off_b = images * kFixU;
-    l.off_sum = l.off_b + kFixStages * kFixB;
+    l.off_sum = l.off_b + stages * kFixB;
     l.off_mask = l.off_sum + tokens * kFixSumRow;
     l.off_adapter = l.off_mask + 128 * 16;
     l.off_bars = l.off_adapter + 128 * 4;
@@ -557,7 +559,8 @@ __host__ __device__ inline FixLayout fix_layout(uint32_t images, uint32_t tokens
 
 // dst[m, 0 .. 64) = the sum of src[b, m, 0 .. 64) over the slots b < n, in order: I chunks of four columns
 // a thread and B slots of each in flight.  For a few tokens that spreads a tile's many slots over threads
-// that had no token (4 tokens, W[4096, 4096], the whole forward: 21.6 to 20.5 us).
+// that had no token (4 tokens, W[4096, 4096], the whole forward: 21.6 to 20.5 us); for many tokens of few slots
+// it is more chunks than slots (112 tokens, W[28672, 8192]: 99.5 to 98 us).
 template <int I, int B>
 __device__ __forceinline__ void sum_slots(const float* src, int64_t slot_floats, int n, int M, int t, char* dst) {
     for (int i0 = t; i0 < M * 16; i0 += 128 * I) {
@@ -593,13 +596,14 @@ __device__ __forceinline__ void sum_slots(const float* src, int64_t slot_floats,
     }
 }
 
-__global__ void __launch_bounds__(kFixThreads)
+__global__ void __launch_bounds__(kFixThreads, kFixCtas)
 tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ CUtensorMap tmB, FixParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - ptx::smem_addr(smem_raw));
     const int images = 2 * p.R / 64;
-    const FixLayout lay = fix_layout((uint32_t)images, p.nt);
+    const FixLayout lay = fix_layout((uint32_t)images, p.nt, (uint32_t)p.stages);
+    const int NS = p.stages;
     const uint32_t sU = base, sB = base + lay.off_b;
     const uint32_t bar_full = base + lay.off_bars, bar_empty = bar_full + 8 * kFixStages;
     const uint32_t bar_u = bar_empty + 8 * kFixStages, bar_acc = bar_u + 8;
@@ -611,7 +615,7 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
 
     for (int i = tid; i < 128 * 4; i += kFixThreads) mask[i] = 0xffffffffu;
     if (tid == 0) {
-        for (int s = 0; s < kFixStages; ++s) {
+        for (int s = 0; s < NS; ++s) {
             ptx::mbar_init(bar_full + 8 * s, 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
@@ -659,11 +663,11 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
                                  bar_full + 8 * s);
             }
             __syncwarp();
-            if (++s == kFixStages) { s = 0; ph ^= 1u; }
+            if (++s == NS) { s = 0; ph ^= 1u; }
         }
         if (*abort) {   // drain this CTA's copies in flight before it exits
-            for (int i = max(0, issued - kFixStages); i < issued; ++i)
-                ptx::mbar_wait_drain(bar_full + 8 * (i % kFixStages), (uint32_t)(i / kFixStages) & 1u);
+            for (int i = max(0, issued - NS); i < issued; ++i)
+                ptx::mbar_wait_drain(bar_full + 8 * (i % NS), (uint32_t)(i / NS) & 1u);
         }
     } else if (warp == 1) {
         const uint32_t idesc = ptx::idesc_set_f16(ptx::idesc_bf16_f32_ab(128, 64, 0, 0), p.f16 != 0);
@@ -697,7 +701,7 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
                 ptx::mma_commit(bar_empty + 8 * s);
             }
             __syncwarp();
-            if (++s == kFixStages) { s = 0; ph ^= 1u; }
+            if (++s == NS) { s = 0; ph ^= 1u; }
         }
         if (ptx::elect_one_sync()) {
             ptx::mma_commit(bar_acc);
@@ -719,8 +723,10 @@ tc_rows_fixup(const __grid_constant__ CUtensorMap tmU2, const __grid_constant__ 
         const bool live = (int)(quad * 32u) < p.M;
         const float* src = p.partial + (int64_t)slot0 * slot_floats + col0;
         char* sums = reinterpret_cast<char*>(gbase + lay.off_sum);
-        if (p.M <= 8) sum_slots<1, 12>(src, slot_floats, sp.y - sp.x + 1, p.M, tid - 64, sums);
-        else sum_slots<4, 4>(src, slot_floats, sp.y - sp.x + 1, p.M, tid - 64, sums);
+        const int slots = sp.y - sp.x + 1;
+        if (p.M <= 8) sum_slots<1, 12>(src, slot_floats, slots, p.M, tid - 64, sums);
+        else if (slots <= 3) sum_slots<6, 3>(src, slot_floats, slots, p.M, tid - 64, sums);
+        else sum_slots<4, 6>(src, slot_floats, slots, p.M, tid - 64, sums);
         asm volatile("bar.sync 1, 128;" ::: "memory");        // the sums of other threads
         const bool acc_ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_acc, 0, abort, p.err));
         ptx::tc_fence_after();
@@ -829,8 +835,21 @@ qlora_status launch_rows(const RowsArgs& a, cudaStream_t stream) {
     CUtensorMap tmU2, tmB;
     if (!make_tmap_2d(&tmU2, true, a.U2, 2 * a.R, a.M, 4 * a.R, 64, 128, true)) return QLORA_ERR_CUDA;
     if (!make_tmap_2d(&tmB, true, a.B, a.ldb, (uint64_t)a.n_adapters * N, a.ldb * 2, 64, 64, true)) return QLORA_ERR_CUDA;
-    (void)launch_dependent(tc_rows_fixup, dim3((unsigned)((N + 63) / 64)), dim3(kFixThreads),
-                           fix_layout((uint32_t)(2 * a.R / 64), f.nt).alloc, stream, tmU2, tmB, f);
+    // As many stages of B as a CTA can use (an adapter's tile takes one for every 64 ranks) and as let all CTAs
+    // run together, at least two; four if no number does (48 tokens, 32 adapters, the whole forward: W[28672, 8192],
+    // 448 CTAs, 105.5 us with four stages and 102 with two; W[8192, 8192] 47.9 with four and 47.4 with sixteen).
+    const int64_t ctas = (N + 63) / 64, tiles = std::min<int64_t>(a.M, a.n_adapters) * ((a.r + 63) / 64);
+    const uint32_t images = (uint32_t)(2 * a.R / 64);
+    f.stages = 4;
+    for (int st = (int)std::min<int64_t>(kFixStages, std::max<int64_t>(2, tiles)); st >= 2; --st) {
+        const uint32_t bytes = fix_layout(images, f.nt, (uint32_t)st).alloc;
+        if (bytes <= kMaxSmem && std::min<int64_t>(kFixCtas, kSmemPerSm / (bytes + 1024)) * sms >= ctas) {
+            f.stages = st;
+            break;
+        }
+    }
+    (void)launch_dependent(tc_rows_fixup, dim3((unsigned)ctas), dim3(kFixThreads),
+                           fix_layout(images, f.nt, (uint32_t)f.stages).alloc, stream, tmU2, tmB, f);
     QLORA_CHECK_LAUNCH();
     return QLORA_OK;
 }
