@@ -8,8 +8,7 @@
 //     loss  = T^2 sum_j p_j (log p_j - (z_{i_j}/T - lse))     (KL divergence, scaled by T^2)
 //     dz_v  = dloss T (exp(z_v/T - lse) - sum_{j: i_j = v} p_j)
 // A row without valid entries (none given, or every t_j = -inf) has loss 0 and gradient 0, and so has a row
-// whose logits are all masked, by -inf or by a type's lowest value (lse below -6e29, far from any logit of
-// a model, where one fp32 number cannot hold both the mask and log V): its lse is -inf.
+// whose logits are all masked (masked_from below): its lse is -inf.
 //
 // Both kernels are bound by HBM: the forward reads every logit once (running maximum and sum of
 // the softmax in registers, fp32, base-2 exponentials), the backward reads and writes every
@@ -110,33 +109,45 @@ __device__ __forceinline__ void store8(void* base, int64_t e, const float (&v)[8
     }
 }
 
-// Running maximum and sum of base-2 exponentials: sum_i 2^(y_i) = s 2^m.  m = -inf stands for an
-// empty sum; the reference subtracted from the exponents is 0 then, so -inf logits add zeros and
-// never meet -inf - -inf.
+// Running maximum and sum of exponentials: sum_i exp(x_i / T) = s 2^(ref(m) c), c = log2(e) / T.  The
+// difference to the maximum is taken before the scaling, so that the largest logit contributes exactly 1 and no
+// exponent is above 0, for logits of any size: with fma(x, c, -r) and r the rounded m c, what r's rounding
+// leaves over exceeds 128 for masks such as -1e10, and a thread of masks only has s = inf.
+// m = -inf stands for an empty sum; the reference is 0 then, so -inf logits add zeros and never meet
+// -inf - -inf.  So it is for +inf, of which s then is.
 struct Softmax2 {
     float m, s;
-    __device__ __forceinline__ static float ref(float m) { return m == -INFINITY ? 0.f : m; }
+    __device__ __forceinline__ static float ref(float m) { return fabsf(m) == INFINITY ? 0.f : m; }
+    __device__ __forceinline__ static float term(float x, float r, float c) {
+        return exp2_approx(__fmul_rn(__fsub_rn(x, r), c));
+    }
     template <int N>
     __device__ __forceinline__ void add(const float (&x)[N], float c) {
-        float top = x[0];
+        float mn = fmaxf(m, x[0]);
 #pragma unroll
-        for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-        const float mn = fmaxf(m, top * c), r = ref(mn);
+        for (int i = 1; i < N; ++i) mn = fmaxf(mn, x[i]);
+        const float r = ref(mn);
         float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            acc0 += exp2_approx(__fmaf_rn(x[i], c, -r));
-            if (i + 1 < N) acc1 += exp2_approx(__fmaf_rn(x[i + 1], c, -r));
+            acc0 += term(x[i], r, c);
+            if (i + 1 < N) acc1 += term(x[i + 1], r, c);
         }
-        s = __fmaf_rn(s, exp2_approx(m - r), acc0 + acc1);
+        s = __fmaf_rn(s, term(m, r, c), acc0 + acc1);
         m = mn;
     }
-    __device__ __forceinline__ void join(float m2, float s2) {
+    __device__ __forceinline__ void join(float m2, float s2, float c) {
         const float mn = fmaxf(m, m2), r = ref(mn);
-        s = s * exp2_approx(m - r) + s2 * exp2_approx(m2 - r);
+        s = s * term(m, r, c) + s2 * term(m2, r, c);
         m = mn;
     }
 };
+
+// A row whose largest logit is not above this is masked throughout: the type's lowest value in fp16, and -1e8
+// in bf16 and fp32, far from any logit of a model, where one fp32 lse cannot hold log V beside the mask
+// (masks of -1e9, -1e10, -1e30, the lowest value).
+template <int DT>
+constexpr float masked_from() { return DT == QLORA_DTYPE_F16 ? -65504.f : -1e8f; }
 
 struct DistillParams {
     const void* logits;       // [M, V], rows ld elements apart
@@ -146,7 +157,7 @@ struct DistillParams {
     const void* t;            // [M, k]
     int32_t t_dtype, k;
     float c;                  // log2(e) / T
-    float T, T2;              // T, T^2
+    float T;
     float* loss;              // [M]            (forward)
     float* lse;               // [M]            (written by the forward, read by the backward)
     const float* dloss;       // [M]            (backward)
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, acc.m, o), s2 = __shfl_xor_sync(0xffffffffu, acc.s, o);
-        acc.join(m2, s2);
+        acc.join(m2, s2, p.c);
     }
     __shared__ float2 warp_acc[kWarps];
     if (part == 0)
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     __syncthreads();
     acc = Softmax2{warp_acc[0].x, warp_acc[0].y};
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) acc.join(warp_acc[w].x, warp_acc[w].y);
+    for (int w = 1; w < kWarps; ++w) acc.join(warp_acc[w].x, warp_acc[w].y, p.c);
     if (p.parts > 1) {                                        // the row's CTAs are one cluster
         cg::cluster_group cluster = cg::this_cluster();
         cluster.barrier_wait();
@@ -283,22 +294,25 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
         cluster.sync();
         if (part != 0) return;
         acc = Softmax2{joined[0].x, joined[0].y};
-        for (int w = 1; w < p.parts; ++w) acc.join(joined[w].x, joined[w].y);
+        for (int w = 1; w < p.parts; ++w) acc.join(joined[w].x, joined[w].y, p.c);
     }
     if (threadIdx.x >= 32) return;                            // one warp ends the row
-    const float lse2 = acc.m + log2f(acc.s);
+    // loss = T sum_e p_e (T (log p_e + log s) - (z_e - ref)): logits only as differences, which the temperature
+    // does not scale up, so that a masked z_e costs its distance and not inf
+    const float ref = Softmax2::ref(acc.m), log_s = log2f(acc.s) * kLn2;
     const Teacher teacher = teacher_softmax(entries, p.k, p.c);
     float sum = 0.f;
     for (int e = threadIdx.x; e < p.k; e += 32) {
         const float lp = log2_p(teacher, entries.t[e], p.c), pe = exp2f(lp);
-        if (entries.i[e] >= 0 && !(pe == 0.f)) sum += pe * (lp - __fmaf_rn(entry_z[e], p.c, -lse2));
+        if (entries.i[e] >= 0 && !(pe == 0.f))
+            sum += pe * __fsub_rn(__fmul_rn(__fmaf_rn(lp, kLn2, log_s), p.T), __fsub_rn(entry_z[e], ref));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const bool masked = lse2 < -1e30f;                        // false for NaN
+    const bool masked = acc.m <= masked_from<DT_IN>() && acc.s == acc.s;   // a NaN, which the maximum skips, is in s
     if (threadIdx.x == 0) {
-        p.lse[m] = masked ? -INFINITY : lse2 * kLn2;
-        p.loss[m] = teacher.some && !masked ? p.T2 * kLn2 * sum : 0.f;
+        p.lse[m] = masked ? -INFINITY : __fdiv_rn(ref, p.T) + log_s;
+        p.loss[m] = teacher.some && !masked ? p.T * sum : 0.f;
     }
 }
 
@@ -463,13 +477,13 @@ qlora_status distill_args(const void* logits, int32_t z_dtype, int64_t ld, int64
     QLORA_TRY(check_elems(idx, 4));
     QLORA_TRY(check_elems(t, elem_size(t_dtype)));
     if (k < 1 || k > kMaxTop) return QLORA_ERR_INVALID_ARG;
-    // 1/T^2 and T^2 stay normal fp32 numbers within these limits
+    // log2(e) / T and T^2 keep their digits and the products with logits their range within these limits
     if (!(T >= 1e-3f && T <= 1e3f)) return QLORA_ERR_INVALID_ARG;
     if (M < 1 || V < 1 || V > INT32_MAX || ld < V || M > INT32_MAX / 8 || ld > (int64_t(1) << 40) / M)
         return QLORA_ERR_SHAPE;
     p.logits = logits; p.ld = ld; p.M = M; p.V = V;
     p.idx = idx; p.t = t; p.t_dtype = t_dtype; p.k = k;
-    p.c = (float)(kLog2e / (double)T); p.T = T; p.T2 = T * T;
+    p.c = (float)(kLog2e / (double)T); p.T = T;
     p.parts = row_parts(M, V);
     return QLORA_OK;
 }

@@ -386,10 +386,13 @@ qlora_status qlora_dequantize_int8_absmax(const int8_t* codes, const float* alph
  *     loss = T^2 sum_j p_j (log p_j - z_{i_j} / T + lse).
  * An index that comes twice is two entries of the same logit.  A row without
  * entries, or whose teacher logits are all -inf, has loss 0.  So has a row whose
- * own logits are all masked, by -inf or a type's lowest value: lse is -inf there.
+ * own logits are all masked, its largest being -inf, z_dtype's lowest value or (fp32
+ * and bf16) -1e8 or less: lse is -inf there.  In other rows a masked logit of any of these
+ * values has probability 0, and a teacher that wants it pays its distance.
  *   logits          device [M, V] of z_dtype (any qlora_dtype), rows ld >= V elements
- *                   apart.  -inf logits have probability 0.  The fp32 lse limits what large
- *                   logits keep: q_v is good to 2^-23 |lse| of itself.
+ *                   apart.  With a +inf logit lse is +inf and every other logit has
+ *                   probability 0 (its own is NaN); a NaN logit makes its row NaN.  The fp32 lse
+ *                   limits what large logits keep: q_v is good to 2^-23 |lse| of itself.
  *   teacher_idx     device int32 [M, k];  1 <= k <= 1024.
  *   teacher_logits  device [M, k] of t_dtype (any qlora_dtype).
  *   temperature     1e-3 .. 1e3.

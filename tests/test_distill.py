@@ -332,3 +332,92 @@ def test_capture_and_replay_on_a_side_stream_with_new_inputs():
         want, want_lse = q4.qlora_distill_topk_fwd(*src[:3], 1.0)
         assert torch.equal(loss, want) and torch.equal(lse, want_lse)
         assert torch.equal(dz, q4.qlora_distill_topk_bwd(*src[:3], want_lse, src[3], 1.0))
+
+
+FINITE_MASKS = [(d, m) for d in (torch.bfloat16, torch.float32) for m in (torch.finfo(d).min, -1e30, -1e10, -1e9)] + \
+    [(torch.float16, torch.finfo(torch.float16).min), (torch.float16, -1e4)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,V", [(6, 40011), (300, 5003)])      # a cluster for each row, a CTA for each row
+@pytest.mark.parametrize("T", [0.7, 1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("dt,mask", FINITE_MASKS)
+def test_finite_masks_count_as_minus_infinity(dt, mask, T, M, V):
+    """A masked prefix, masked leading chunks, all but a few scattered logits masked, every second logit
+    masked: threads that meet only masks, first or throughout.  exp(mask / T) is 0 in fp64 too, so the
+    formula of -inf logits is the reference, with the tolerance of the logits that are left."""
+    z, idx, t, dloss = make(M, V, 9, dt, torch.float32, seed=21)
+    masked = torch.zeros(M, V, dtype=torch.bool, device="cuda")
+    at = torch.arange(V, device="cuda")
+    masked[0::6] = at < V // 2
+    masked[1::6] = at < V - 20
+    masked[2::6] = (at != 17) & (at != V // 3) & (at != V - 2)
+    masked[3::6] = at % 2 == 0
+    masked[4::6] = at >= 5
+    left = [torch.nonzero(~masked[m])[:, 0] for m in range(6)]
+    for m in range(M):                                           # the teacher's entries are logits that are left
+        idx[m] = torch.where(idx[m] < 0, idx[m], left[m % 6][(idx[m] % len(left[m % 6])).long()].int())
+    z = z.masked_fill(masked, mask)
+    zs = z.masked_fill(masked, -math.inf)
+    ref_loss, ref_lse, ref_dz, mag = formulas(zs, idx, t, T, dloss)
+    e = unit(zs, t, idx, T, V)
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, T)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, T, d_dtype=torch.float32)
+    assert torch.all((lse.double().cpu() - ref_lse).abs() <= e * (1 + ref_lse.abs()))
+    assert torch.all((loss.double().cpu() - ref_loss).abs() <= 2 * e * (T * T + mag) + 2.0 ** -23 * ref_loss.abs())
+    q = (zs.double().cpu() / T - ref_lse[:, None]).exp() * T * dloss.double().cpu()[:, None]
+    tol = 4 * e * (q + (q - ref_dz).abs()) + 2.0 ** -24 * ref_dz.abs() + 1e-37
+    assert torch.all((dz.double().cpu() - ref_dz).abs() <= tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [9, 30011])
+@pytest.mark.parametrize("T", [0.7, 1.0, 1.5, 2.0, 4.0, 30.0])
+@pytest.mark.parametrize("dt,mask", [c for c in FINITE_MASKS if c[1] != -1e4])
+def test_rows_masked_throughout_by_any_mask(dt, mask, T, V):
+    z, idx, t, dloss = make(3, V, 4, dt, torch.float32, seed=4)
+    idx[:, 0] = 1
+    z[0] = mask
+    z[1, ::2], z[1, 1::2] = mask, -math.inf
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, T)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, dloss, T)
+    assert torch.all(lse[:2] == -math.inf) and torch.all(loss[:2] == 0) and torch.all(dz[:2] == 0)
+    assert torch.isfinite(lse[2]) and torch.isfinite(loss[2]) and torch.any(dz[2] != 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [0.7, 1.0, 1.5])
+@pytest.mark.parametrize("dt,mask", [c for c in FINITE_MASKS if c[0] != torch.float16])
+def test_the_teachers_weight_on_a_masked_logit_costs_its_distance(dt, mask, T):
+    """Half of the teacher's weight on a logit at the mask: the loss is T p (z_max - mask) and small terms, finite
+    in fp32 for these T although mask / T^2 may not be.  p, its product and the sum are each rounded, and the
+    approximation of p is off by 2^-22: 2^-20 in all, of a loss of at least 0.5 T |mask|."""
+    V = 3000
+    z, _, _, _ = make(2, V, 2, dt, torch.float32, seed=2)
+    z[:, 100:] = mask
+    idx = torch.tensor([[5, 2000], [2500, 7]], dtype=torch.int32, device="cuda")
+    t = torch.zeros(2, 2, device="cuda")
+    ref = formulas(z, idx, t, T, torch.ones(2))[0]
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, T)
+    assert torch.isfinite(ref.float()).all() and torch.isfinite(lse).all()
+    assert torch.all((loss.double().cpu() - ref).abs() <= 2.0 ** -20 * ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,V", [(2, 9), (2, 40011), (300, 5003)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+def test_a_logit_of_plus_infinity_has_the_whole_row(dt, M, V):
+    """lse is +inf as logsumexp has it; every other logit has probability 0, so a teacher that wants one of them
+    has a loss of +inf and the gradient -p there; inf - inf on the logit itself is NaN.  A NaN in the row wins."""
+    z, _, _, _ = make(M, V, 1, dt, torch.float32, seed=6)
+    idx = torch.full((M, 1), 2, dtype=torch.int32, device="cuda")
+    t, one = torch.zeros(M, 1, device="cuda"), torch.ones(M, device="cuda")
+    z[0, V - 4] = math.inf
+    z[1, V - 4], z[1, 0] = math.inf, math.nan
+    loss, lse = q4.qlora_distill_topk_fwd(z, idx, t, 2.0)
+    dz = q4.qlora_distill_topk_bwd(z, idx, t, lse, one, 2.0)
+    assert lse[0] == math.inf and loss[0] == math.inf and lse[1].isnan() and loss[1].isnan()
+    want = torch.zeros(V, device="cuda")
+    want[2], want[V - 4] = -2.0, math.nan
+    assert torch.equal(dz[0].float().nan_to_num(9.0), want.nan_to_num(9.0)) and dz[1].isnan().all()
+    assert torch.isfinite(lse[2:]).all() and torch.isfinite(dz[2:]).all()
