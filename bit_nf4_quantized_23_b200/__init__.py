@@ -6,9 +6,16 @@ The Python functions below carry the names of the C entry points of libqlora.so
 torch (device memory), pass raw pointers and the current CUDA stream, and check
 the returned status.  Every step of the computation runs in the library's CUDA
 kernels; there is no CPU or PyTorch fallback.
+
+`stream=` runs a call on another stream than the current one.  What the caller passes
+has to be ready for that stream, and what comes back is complete when it is (as for any
+work on a stream of one's own: wait_stream before and after).  Workspaces and outputs that
+the call allocates belong to that stream; the outputs are also marked as used by the
+current one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from ctypes import byref, c_float, c_size_t, c_uint32
 from dataclasses import dataclass
@@ -33,6 +40,37 @@ __all__ = [
 def _stream(stream) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _allocating_on(stream):
+    """A context in which torch allocates for `stream` (None: the current one).  The caching allocator hands
+    out a block again in the order of the stream that it was allocated on, so memory that the kernels on
+    `stream` use has to come from there, or another call could have it while they still run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _for_current(t: torch.Tensor, stream) -> torch.Tensor:
+    """An output allocated on `stream`, which the current stream is going to use too."""
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with _allocating_on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _output(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating_on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return _for_current(t, stream)
 
 
 def _ptr(t):
@@ -170,9 +208,13 @@ def qlora_quantize_nf4_dq(W: torch.Tensor, blocksize: int = 64, blocksize2: int 
     N, K = W.shape
     sizes = qlora_nf4_sizes(N, K, blocksize, blocksize2)
     if out is None:
-        out = NF4Weight.empty(N, K, W.device, codebook, double_quant, compute_dtype)
+        with _allocating_on(stream):
+            out = NF4Weight.empty(N, K, W.device, codebook, double_quant, compute_dtype)
+        for name in out._BUFFERS:
+            if getattr(out, name) is not None:
+                _for_current(getattr(out, name), stream)
     if workspace is None:
-        workspace = torch.empty(sizes["workspace"], dtype=torch.uint8, device=W.device)
+        workspace = _scratch(sizes["workspace"], W.device, stream)
     ws = out.c_struct()
     check(lib().qlora_quantize_nf4_dq(_ptr(W), N, K, blocksize, blocksize2, byref(ws), _ptr(workspace),
                                       workspace.numel(), _stream(stream)), "qlora_quantize_nf4_dq")
@@ -193,7 +235,7 @@ def qlora_quantize_nf4_dq_noalloc(W: torch.Tensor, out: NF4Weight, stream=None) 
 
 def qlora_dequantize(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     if out is None:
-        out = torch.empty(w.N, w.K, dtype=w.compute_dtype, device=w.codes.device)
+        out = _output((w.N, w.K), w.compute_dtype, w.codes.device, stream)
     _need(out, w.compute_dtype, "out", (w.N, w.K))
     ws = w.c_struct()
     check(lib().qlora_dequantize(byref(ws), _ptr(out), _stream(stream)), "qlora_dequantize")
@@ -208,9 +250,9 @@ def qlora_quantize_int8_absmax(W: torch.Tensor, blocksize: int = 64, codes: torc
     _need(W, torch.bfloat16, "W")
     n = W.numel()
     if codes is None:
-        codes = torch.empty(W.shape, dtype=torch.int8, device=W.device)
+        codes = _output(W.shape, torch.int8, W.device, stream)
     if alpha is None:
-        alpha = torch.empty(max(n // blocksize, 1), dtype=torch.float32, device=W.device)
+        alpha = _output((max(n // blocksize, 1),), torch.float32, W.device, stream)
     _need(codes, torch.int8, "codes", tuple(W.shape))
     _need(alpha, torch.float32, "alpha")
     if blocksize <= 0 or alpha.numel() * blocksize != n:
@@ -228,7 +270,7 @@ def qlora_dequantize_int8_absmax(codes: torch.Tensor, alpha: torch.Tensor, block
     if blocksize <= 0 or alpha.numel() * blocksize != codes.numel():
         raise ValueError(f"alpha must hold codes.numel() / blocksize = {codes.numel() // max(blocksize, 1)} scales")
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        out = _output(codes.shape, dtype, codes.device, stream)
     _need(out, dtype, "out", tuple(codes.shape))
     check(lib().qlora_dequantize_int8_absmax(_ptr(codes), _ptr(alpha), codes.numel(), blocksize, _ptr(out),
                                              _dtype_code(dtype), _stream(stream)), "qlora_dequantize_int8_absmax")
@@ -242,7 +284,7 @@ def qlora_merge_lora(w: NF4Weight, A: torch.Tensor, B: torch.Tensor, r: int, alp
     _need(A, w.compute_dtype, "A", (r, w.K))
     _need(B, w.compute_dtype, "B", (w.N, r))
     if out is None:
-        out = torch.empty(w.N, w.K, dtype=w.compute_dtype, device=w.codes.device)
+        out = _output((w.N, w.K), w.compute_dtype, w.codes.device, stream)
     _need(out, w.compute_dtype, "out", (w.N, w.K))
     ws = w.c_struct()
     check(lib().qlora_merge_lora(byref(ws), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream)),
@@ -256,11 +298,9 @@ def qlora_linear_workspace_size(M: int, N: int, K: int, r: int) -> int:
     return n.value
 
 
-def _workspace(M, N, K, r, device, workspace):
+def _workspace(M, N, K, r, device, workspace, stream):
     need = qlora_linear_workspace_size(M, N, K, r)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return workspace
+    return _scratch(max(need, 16), device, stream) if workspace is None else workspace
 
 
 def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, r: int,
@@ -275,13 +315,13 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
     _need(A, w.compute_dtype, "A", (r, w.K))
     _need(B, w.compute_dtype, "B", (w.N, r))
     if out is None:
-        out = torch.empty(M, w.N, dtype=y_dtype, device=X.device)
+        out = _output((M, w.N), y_dtype, X.device, stream)
     _need(out, y_dtype, "Y", (M, w.N))
     if save_U and U_out is None:
-        U_out = torch.empty(M, r, dtype=torch.float32, device=X.device)
+        U_out = _output((M, r), torch.float32, X.device, stream)
     if U_out is not None:
         _need(U_out, torch.float32, "U", (M, r))
-    workspace = _workspace(M, w.N, w.K, r, X.device, workspace)
+    workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
     ws = w.c_struct()
     check(lib().qlora_linear_fwd(byref(ws), _ptr(X), M, _ptr(A), _ptr(B), r, c_float(alpha), _ptr(out),
                                  _dtype_code(y_dtype), _ptr(U_out), _ptr(workspace), workspace.numel(),
@@ -304,10 +344,10 @@ def qlora_linear_fwd_multi(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor, B
     _need(B_all, w.compute_dtype, "B_all", (n_ad, w.N, r))
     _need(adapter_idx, torch.int32, "adapter_idx", (M,))
     if out is None:
-        out = torch.empty(M, w.N, dtype=y_dtype, device=X.device)
+        out = _output((M, w.N), y_dtype, X.device, stream)
     _need(out, y_dtype, "Y", (M, w.N))
-    U = torch.empty(M, r, dtype=torch.float32, device=X.device) if save_U else None
-    workspace = _workspace(M, w.N, w.K, r, X.device, workspace)
+    U = _output((M, r), torch.float32, X.device, stream) if save_U else None
+    workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
     ws = w.c_struct()
     check(lib().qlora_linear_fwd_multi(byref(ws), _ptr(X), M, _ptr(A_all), _ptr(B_all), n_ad, _ptr(adapter_idx),
                                        r, c_float(alpha), _ptr(out), _dtype_code(y_dtype), _ptr(U),
@@ -331,16 +371,16 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     if U_saved is not None:
         _need(U_saved, torch.float32, "U_saved", (M, r))
     if need_dX and dX is None:
-        dX = torch.empty(M, w.K, dtype=dx_dtype, device=X.device)
+        dX = _output((M, w.K), dx_dtype, X.device, stream)
     if dX is not None:
         _need(dX, dx_dtype, "dX", (M, w.K))
     if dA is None:
-        dA = torch.empty(r, w.K, dtype=torch.float32, device=X.device)
+        dA = _output((r, w.K), torch.float32, X.device, stream)
     if dB is None:
-        dB = torch.empty(w.N, r, dtype=torch.float32, device=X.device)
+        dB = _output((w.N, r), torch.float32, X.device, stream)
     _need(dA, torch.float32, "dA", (r, w.K))
     _need(dB, torch.float32, "dB", (w.N, r))
-    workspace = _workspace(M, w.N, w.K, r, X.device, workspace)
+    workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
     ws = w.c_struct()
     check(lib().qlora_linear_bwd(byref(ws), _ptr(X), _ptr(dY), M, _ptr(A), _ptr(B), r, c_float(alpha),
                                  _ptr(U_saved), _ptr(dX), _dtype_code(dx_dtype), _ptr(dA), _ptr(dB),
@@ -388,7 +428,7 @@ def qlora_adapters_workspace_size(M: int, N: int, K: int, r: int, n_adapters: in
     return n.value
 
 
-def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev):
+def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, stream):
     """Checks of both directions; returns (M, n_adapters, r, addresses in C order, workspace)."""
     if not isinstance(A_all, torch.Tensor) or A_all.dim() != 3:
         raise ValueError("A_all must be 3-D [n_adapters, r, K]")
@@ -399,7 +439,7 @@ def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev):
     if w.codes.get_device() != dev:
         raise ValueError(f"the weight must be on the current CUDA device cuda:{dev}, got {w.codes.device}")
     if workspace is None:
-        workspace = torch.empty(qlora_adapters_workspace_size(M, w.N, w.K, r, n), dtype=torch.uint8, device=X.device)
+        workspace = _scratch(qlora_adapters_workspace_size(M, w.N, w.K, r, n), X.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on the current CUDA device cuda:{dev}")
     return M, n, r, at, workspace
@@ -415,13 +455,13 @@ def qlora_linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor
     adapter_idx int32 [M], scales fp32 [n], all on the current device.  Returns (Y, U) with U fp32
     [M, r] (or None)."""
     dev = _device_of(X, "X")
-    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev)
+    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, stream)
     y_dtype = w.compute_dtype if y_dtype is None else y_dtype
     if out is None:
-        out = torch.empty((M, w.N), dtype=y_dtype, device=X.device)
+        out = _output((M, w.N), y_dtype, X.device, stream)
     y_at = _need_on(out, y_dtype, "Y", (M, w.N), dev)
     if save_U and U_out is None:
-        U_out = torch.empty((M, r), dtype=torch.float32, device=X.device)
+        U_out = _output((M, r), torch.float32, X.device, stream)
     u_at = None if U_out is None else _need_on(U_out, torch.float32, "U", (M, r), dev)
     check(lib().qlora_linear_fwd_adapters(byref(w.c_struct()), at[0], M, at[1], at[2], n, at[3], r, at[4], y_at,
                                           _dtype_code(y_dtype), u_at, workspace.data_ptr(), workspace.numel(),
@@ -437,17 +477,17 @@ def qlora_linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A
     """(dX, dA_all, dB_all) of <dY, Y> of qlora_linear_fwd_adapters: dA_all fp32 [n, r, K] and dB_all
     fp32 [n, N, r] hold every adapter's gradient over its own tokens.  dX is None when need_dX is False."""
     dev = _device_of(X, "X")
-    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev)
+    M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, stream)
     dx_dtype = w.compute_dtype if dx_dtype is None else dx_dtype
     dy_at = _need_on(dY, w.compute_dtype, "dY", (M, w.N), dev)
     u_at = None if U_saved is None else _need_on(U_saved, torch.float32, "U_saved", (M, r), dev)
     if need_dX and dX is None:
-        dX = torch.empty((M, w.K), dtype=dx_dtype, device=X.device)
+        dX = _output((M, w.K), dx_dtype, X.device, stream)
     dx_at = None if dX is None else _need_on(dX, dx_dtype, "dX", (M, w.K), dev)
     if dA is None:
-        dA = torch.empty((n, r, w.K), dtype=torch.float32, device=X.device)
+        dA = _output((n, r, w.K), torch.float32, X.device, stream)
     if dB is None:
-        dB = torch.empty((n, w.N, r), dtype=torch.float32, device=X.device)
+        dB = _output((n, w.N, r), torch.float32, X.device, stream)
     da_at = _need_on(dA, torch.float32, "dA", (n, r, w.K), dev)
     db_at = _need_on(dB, torch.float32, "dB", (n, w.N, r), dev)
     check(lib().qlora_linear_bwd_adapters(byref(w.c_struct()), at[0], dy_at, M, at[1], at[2], n, at[3], r, at[4], u_at,
@@ -501,9 +541,9 @@ def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
     z_code, ld, k, t_code, i_at, t_at = _topk_args(logits, teacher_idx, teacher_logits, dev)
     M, V = logits.shape
     if loss is None:
-        loss = torch.empty(M, dtype=torch.float32, device=logits.device)
+        loss = _output((M,), torch.float32, logits.device, stream)
     if lse is None:
-        lse = torch.empty(M, dtype=torch.float32, device=logits.device)
+        lse = _output((M,), torch.float32, logits.device, stream)
     check(lib().qlora_distill_topk_fwd(logits.data_ptr(), z_code, ld, M, V, i_at, t_at, t_code, k, temperature,
                                        _need_on(loss, torch.float32, "loss", (M,), dev),
                                        _need_on(lse, torch.float32, "lse", (M,), dev), _stream_on(stream, dev)),
@@ -522,7 +562,7 @@ def qlora_distill_topk_bwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
     lse_at = _need_on(lse, torch.float32, "lse", (M,), dev)
     dloss_at = _need_on(dloss, torch.float32, "dloss", (M,), dev)
     if dlogits is None:
-        dlogits = torch.empty((M, V), dtype=logits.dtype if d_dtype is None else d_dtype, device=logits.device)
+        dlogits = _output((M, V), logits.dtype if d_dtype is None else d_dtype, logits.device, stream)
     elif d_dtype is not None and dlogits.dtype != d_dtype:
         raise TypeError(f"dlogits must be {d_dtype}, got {dlogits.dtype}")
     d_code, ldd = _rows(dlogits, "dlogits", dev, (M, V))
