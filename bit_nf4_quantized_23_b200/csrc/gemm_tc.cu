@@ -1590,8 +1590,8 @@ qlora_status launch_tc_gemm_nf4(TcGemmArgs& a, bool dx, cudaStream_t stream) {
             QLORA_CHECK_LAUNCH();
             return QLORA_OK;
         }
-        if (bm == 256) return dx ? launch_one<2, true, true>(a, stream) : launch_one<2, false, true>(a, stream);
-        return dx ? launch_one<1, true, true>(a, stream) : launch_one<1, false, true>(a, stream);
+        if (!dx) return launch_one<2, false, true>(a, stream);    // up to kRowsMaxM tokens have kernels of their own
+        return bm == 256 ? launch_one<2, true, true>(a, stream) : launch_one<1, true, true>(a, stream);
     }
     if (pair) return dx ? launch_pair<true, false>(a, stream) : launch_pair<false, false>(a, stream);
     if (bm == 256) return dx ? launch_one<2, true, false>(a, stream) : launch_one<2, false, false>(a, stream);
