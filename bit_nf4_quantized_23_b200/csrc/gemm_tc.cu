@@ -1321,15 +1321,28 @@ static qlora_status launch_pair(const TcGemmArgs& a, cudaStream_t stream, int sp
     return QLORA_OK;
 }
 
-// Whether the forward and dX run on CTA pairs: more than 256 tokens (a pair's tile covers 512),
-// unless the environment variable QLORA_PAIR_GEMM is set to 0 (the single-CTA kernels then run).
-static bool use_pairs(int64_t M) {
+// The environment variable QLORA_PAIR_GEMM set to 0: the forward and dX, with one adapter or many, run on the
+// single-CTA kernels throughout.
+static bool pairs_enabled() {
     static const bool enabled = [] {
         const char* e = std::getenv("QLORA_PAIR_GEMM");
         return !(e && e[0] == '0');
     }();
-    return enabled && M > 256;
+    return enabled;
 }
+
+// QLORA_PAIR_BN=256|240|224 forces the width of the forward's pair tiles (tuning override); 0: chosen.
+static int forced_pair_width() {
+    static const int forced = [] {
+        const char* e = std::getenv("QLORA_PAIR_BN");
+        const int v = e ? std::atoi(e) : 0;
+        return (v == 256 || v == 240 || v == 224) ? v : 0;
+    }();
+    return forced;
+}
+
+// Whether the forward and dX run on CTA pairs: more than 256 tokens (a pair's tile covers 512).
+static bool use_pairs(int64_t M) { return pairs_enabled() && M > 256; }
 
 // Forward pair-tile width: the multiple of 16 in {256, 240, 224} that minimises waves x width,
 // the time of the launch when every pair runs one tile at a time (ties to the wider tile), with
@@ -1362,12 +1375,7 @@ static int pair_tile_width(int64_t M, int64_t N) {
         }
         slots = n;
     }
-    static const int forced = [] {   // QLORA_PAIR_BN=256|240|224 forces the width (tuning override)
-        const char* e = std::getenv("QLORA_PAIR_BN");
-        const int v = e ? std::atoi(e) : 0;
-        return (v == 256 || v == 240 || v == 224) ? v : 0;
-    }();
-    if (forced) return forced;
+    if (forced_pair_width()) return forced_pair_width();
     const int64_t mtiles = (M + 511) / 512;
     int best = kBN;
     int64_t best_cost = INT64_MAX;
@@ -1395,8 +1403,10 @@ struct AdaptersPlan {
 static AdaptersPlan adapters_plan(int64_t M, int64_t Nout, int64_t red, bool dx) {
     const int64_t steps = (red + 63) / 64;
     AdaptersPlan best = {false, kBN, 1};
+    if (!pairs_enabled()) return best;
     double best_ns = M > 256 ? 1e300 : 1000.0 * (double)(((Nout + kBN - 1) / kBN + 147) / 148 * steps);
-    for (int bn : {256, 224, 192, 160}) {
+    for (int width : {256, 224, 192, 160}) {
+        const int bn = !dx && forced_pair_width() ? forced_pair_width() : width;
         const int64_t pairs = (M + 511) / 512 * ((Nout + bn - 1) / bn);
         const int64_t most = std::max<int64_t>(1, std::min<int64_t>(74 / pairs, steps / 16));
         for (int64_t want = 1; want <= most; ++want) {
@@ -1405,7 +1415,7 @@ static AdaptersPlan adapters_plan(int64_t M, int64_t Nout, int64_t red, bool dx)
                               (splits > 1 ? 3000.0 + 0.0016 * (double)(M * Nout * splits) : 0.0);
             if (ns < best_ns) { best_ns = ns; best = {true, bn, (int)splits}; }
         }
-        if (dx) break;
+        if (bn != width || dx) break;
     }
     return best;
 }

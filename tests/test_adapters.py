@@ -538,3 +538,42 @@ def test_need_dX_false_and_a_chain_through_the_distillation_loss():
     # the difference quotient's own error is below h^2
     bound = float((c.dY.double().cpu().abs().t() @ U.double().cpu().abs()).mul(D.abs().amax(0) * s.max()).sum()) * 2.0 ** -8
     assert abs(num - got) <= bound + 1e-5, (num, got, bound)
+
+
+def _with_switch(code, **env):
+    """Standard output of `code` in a process of its own, since the switches are read once."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    root = os.path.dirname(tests)
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=600,
+                         env={**os.environ, "PYTHONPATH": os.pathsep.join([root, tests]), **env})
+    assert res.returncode == 0, res.stderr[-2000:]
+    return res.stdout
+
+
+def test_the_switch_to_single_cta_kernels_covers_the_adapter_calls():
+    """200 tokens through W[8192, 8192] split the reduction over pairs, for which the workspace holds fp32
+    partial outputs; with QLORA_PAIR_GEMM=0 there are none (on the host: the size is all that is asked)."""
+    code = ("import bit_nf4_quantized_23_b200 as q4; "
+            "print(q4.qlora_adapters_workspace_size(200, 8192, 8192, 16, 4), q4.qlora_adapters_workspace_size(2, 64, 64, 16, 4))")
+    with_pairs, without = (_with_switch(code, QLORA_PAIR_GEMM=v).split() for v in ("1", "0"))
+    assert int(with_pairs[0]) - int(without[0]) >= 2 * 200 * 8192 * 4
+    assert with_pairs[1] == without[1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("env", [dict(QLORA_PAIR_GEMM="0"), dict(QLORA_PAIR_BN="240"), dict(QLORA_PAIR_BN="224")])
+def test_results_under_the_switches(env):
+    code = """
+import torch
+from test_adapters import BF16, F16, F32, Case, check
+for shape in [(100, 136, 256, 16, 4), (129, 300, 192, 40, 3), (256, 264, 192, 16, 30), (300, 520, 1088, 96, 5),
+              (513, 523, 640, 24, 7), (1100, 280, 128, 256, 3)]:
+    for rows in ("runs", "mixed"):
+        check(Case(*shape, rows))
+check(Case(700, 264, 384, 64, 3, "mixed", dt=F16), F32)
+print("as the formulas")
+"""
+    assert "as the formulas" in _with_switch(code, **env)
