@@ -577,3 +577,12 @@ check(Case(700, 264, 384, 64, 3, "mixed", dt=F16), F32)
 print("as the formulas")
 """
     assert "as the formulas" in _with_switch(code, **env)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,r,n", [(200, 20000, 128, 16, 5), (256, 28672, 64, 40, 3), (100, 136, 20032, 8, 4),
+                                       (129, 72, 20032, 33, 3), (256, 200, 22016, 64, 6)])
+@pytest.mark.parametrize("rows", ["runs", "mixed"])
+def test_wide_outputs_of_up_to_256_tokens(M, N, K, r, n, rows):
+    """75 to 148 tiles of 256 columns: one wave of single CTAs, which these products take, or two of pairs."""
+    check(Case(M, N, K, r, n, rows, seed=9))
