@@ -42,31 +42,35 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _is_current(stream) -> bool:
+    return stream is None or stream.cuda_stream == torch.cuda.current_stream().cuda_stream
+
+
 def _allocating_on(stream):
     """A context in which torch allocates for `stream` (None: the current one).  The caching allocator hands
     out a block again in the order of the stream that it was allocated on, so memory that the kernels on
     `stream` use has to come from there, or another call could have it while they still run."""
-    if stream is None:
+    if _is_current(stream):
         return contextlib.nullcontext()
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def _for_current(t: torch.Tensor, stream) -> torch.Tensor:
     """An output allocated on `stream`, which the current stream is going to use too."""
-    if stream is not None:
+    if not _is_current(stream):
         t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    if stream is None:
+    if _is_current(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with _allocating_on(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _output(shape, dtype, device, stream) -> torch.Tensor:
-    if stream is None:
+    if _is_current(stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with _allocating_on(stream):
         t = torch.empty(shape, dtype=dtype, device=device)

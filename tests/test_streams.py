@@ -41,7 +41,8 @@ def calls(w, z):
 
 
 class FakeStream:
-    cuda_stream = 7
+    def __init__(self, at):
+        self.cuda_stream = at
 
 
 @pytest.mark.parametrize("name", sorted(calls(None, lambda s, d: torch.zeros(s, dtype=d))))
@@ -74,11 +75,12 @@ def test_what_a_call_allocates_belongs_to_its_stream(name, monkeypatch):
     monkeypatch.setattr(q4, "lib", Library)
     monkeypatch.setattr(q4, "_need", lambda *a: None)
     monkeypatch.setattr(q4, "_device_of", lambda *a: -1)
+    monkeypatch.setattr(q4, "_raw_stream", None)
     monkeypatch.setattr(torch, "empty", counted)
     monkeypatch.setattr(torch.cuda, "stream", stream_context)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "current")
+    current, s = FakeStream(3), FakeStream(7)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
-    s = FakeStream()
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at: s if at == 7 else None)
     got = call(stream=s)
     assert allocated and len(launched) == 1
@@ -86,7 +88,13 @@ def test_what_a_call_allocates_belongs_to_its_stream(name, monkeypatch):
     if isinstance(got, q4.NF4Weight):
         got = [getattr(got, b) for b in got._BUFFERS]
     returned = [t for t in (got if isinstance(got, (tuple, list)) else (got,)) if t is not None]
-    assert sorted(recorded) == sorted((t.data_ptr(), "current") for t in returned)
+    assert sorted(p for p, _ in recorded) == sorted(t.data_ptr() for t in returned)
+    assert all(by is current for _, by in recorded)
+    # the current stream, named or not: allocated as ever
+    for same in (dict(), dict(stream=current)):
+        allocated.clear(), recorded.clear()
+        call(**same)
+        assert allocated and all(at is None for at, _ in allocated) and not recorded
 
 
 @pytest.mark.gpu
