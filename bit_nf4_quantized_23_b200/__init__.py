@@ -434,7 +434,9 @@ def qlora_adapters_workspace_size(M: int, N: int, K: int, r: int, n_adapters: in
 
 def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, stream):
     """Checks of both directions; returns (M, n_adapters, r, addresses in C order, workspace)."""
-    if not isinstance(A_all, torch.Tensor) or A_all.dim() != 3:
+    if not isinstance(A_all, torch.Tensor):
+        raise TypeError("A_all must be a torch.Tensor")
+    if A_all.dim() != 3:
         raise ValueError("A_all must be 3-D [n_adapters, r, K]")
     M, (n, r, _), dt = X.shape[0], A_all.shape, w.compute_dtype
     at = (_need_on(X, dt, "X", (M, w.K), dev), _need_on(A_all, dt, "A_all", (n, r, w.K), dev),
@@ -444,6 +446,8 @@ def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, strea
         raise ValueError(f"the weight must be on the current CUDA device cuda:{dev}, got {w.codes.device}")
     if workspace is None:
         workspace = _scratch(qlora_adapters_workspace_size(M, w.N, w.K, r, n), X.device, stream)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on the current CUDA device cuda:{dev}")
     return M, n, r, at, workspace
@@ -523,7 +527,10 @@ def _rows(t: torch.Tensor, name: str, dev: int, shape=None):
 
 def _topk_args(logits, teacher_idx, teacher_logits, dev):
     z_code, ld = _rows(logits, "logits", dev)
-    if not isinstance(teacher_idx, torch.Tensor) or teacher_idx.dim() != 2:
+    for t, name in ((teacher_idx, "teacher_idx"), (teacher_logits, "teacher_logits")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if teacher_idx.dim() != 2:
         raise ValueError("teacher_idx must be a 2-D tensor [M, k]")
     k = teacher_idx.shape[1]
     shape, t_dtype = (logits.shape[0], k), teacher_logits.dtype

@@ -586,3 +586,17 @@ print("as the formulas")
 def test_wide_outputs_of_up_to_256_tokens(M, N, K, r, n, rows):
     """75 to 148 tiles of 256 columns: one wave of single CTAs, which these products take, or two of pairs."""
     check(Case(M, N, K, r, n, rows, seed=9))
+
+
+def test_what_is_no_tensor_is_a_type_error(monkeypatch):
+    w = q4.NF4Weight.empty(48, 128, device="cpu")
+    X, dY, A, B = (torch.zeros(s, dtype=BF16) for s in ((5, 128), (5, 48), (2, 8, 128), (2, 48, 8)))
+    idx, scales = torch.zeros(5, dtype=torch.int32), torch.ones(2)
+    monkeypatch.setattr(q4, "_device_of", lambda *a: -1)         # lets tensors of the host past the first check
+    good = dict(A_all=A, B_all=B, adapter_idx=idx, scales=scales)
+    for name in [*good, "workspace"]:
+        args = {**good, name: 3}
+        with pytest.raises(TypeError, match=name + " must be a torch.Tensor"):
+            q4.qlora_linear_fwd_adapters(w, X, **args)
+        with pytest.raises(TypeError, match=name + " must be a torch.Tensor"):
+            q4.qlora_linear_bwd_adapters(w, X, dY, **args)

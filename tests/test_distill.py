@@ -421,3 +421,13 @@ def test_a_logit_of_plus_infinity_has_the_whole_row(dt, M, V):
     want[2], want[V - 4] = -2.0, math.nan
     assert torch.equal(dz[0].float().nan_to_num(9.0), want.nan_to_num(9.0)) and dz[1].isnan().all()
     assert torch.isfinite(lse[2:]).all() and torch.isfinite(dz[2:]).all()
+
+
+def test_what_is_no_tensor_is_a_type_error(monkeypatch):
+    z, i, t, v = torch.zeros(2, 8), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2)
+    monkeypatch.setattr(q4, "_device_of", lambda *a: -1)         # lets tensors of the host past the first check
+    for bad in ((z, i, [[0.0] * 3] * 2), (z, [[0] * 3] * 2, t), (z, i, None)):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            q4.qlora_distill_topk_fwd(*bad)
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            q4.qlora_distill_topk_bwd(*bad, v, v)
