@@ -174,7 +174,7 @@ def _code_only(text: str) -> str:
 
 # The fused dequant-GEMM's sources: its device and launch code, its parameter structs, the PTX
 # wrappers and the shared helpers it is compiled from.
-FUSED_GEMM_SOURCES = ("gemm_tc.cu", "gemm_tc.cuh", "qlora_internal.cuh", "tc_ptx.cuh")
+FUSED_GEMM_SOURCES = ("gemm_tc.cu", "gemm_tc.cuh", "nf4_expand.cuh", "qlora_internal.cuh", "tc_ptx.cuh")
 
 
 def kernel_source_sha(files=FUSED_GEMM_SOURCES):

@@ -47,3 +47,17 @@ def test_recorded_traffic_is_keyed_on_the_current_sources(bench):
     for kind in ("fwd_main", "dx_main"):
         v = bench.recorded_traffic(kind)
         assert v is None or v > 0
+
+
+def test_the_source_hash_covers_every_header_that_the_fused_gemm_includes(bench):
+    import re
+    csrc = os.path.join(ROOT, "bit_nf4_quantized_23_b200", "csrc")
+    found, todo = set(), ["gemm_tc.cu"]
+    while todo:
+        name = todo.pop()
+        if name in found:
+            continue
+        found.add(name)
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            todo += [h for h in re.findall(r'#include "([^"]+)"', f.read()) if os.path.exists(os.path.join(csrc, h)) and "/" not in h]
+    assert found == set(bench.FUSED_GEMM_SOURCES)
