@@ -41,6 +41,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Two additions in one instruction, each rounded as __fadd_rn.
+__device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 template <int DT>
 __device__ __forceinline__ float load1(const void* base, int64_t e) {
     if constexpr (DT == QLORA_DTYPE_F32) return static_cast<const float*>(base)[e];
@@ -121,7 +131,10 @@ struct Softmax2 {
     __device__ __forceinline__ static float term(float x, float r, float c) {
         return exp2_approx(__fmul_rn(__fsub_rn(x, r), c));
     }
-    template <int N>
+    // PAIRS: differences and products two at a time, the same values.  For logits of 16 bits (a call at
+    // [4096, 128000] bf16: 186.2 us, one by one 188.5); fp32 logits leave no registers for it (the kernel at
+    // [1023, 50001]: 41.2 us in pairs, 38.8 one by one).
+    template <bool PAIRS, int N>
     __device__ __forceinline__ void add(const float (&x)[N], float c) {
         float mn = fmaxf(m, x[0]);
 #pragma unroll
@@ -130,8 +143,14 @@ struct Softmax2 {
         float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            acc0 += term(x[i], r, c);
-            if (i + 1 < N) acc1 += term(x[i + 1], r, c);
+            if constexpr (PAIRS) {
+                const float2 y = mul2_rn(add2_rn(make_float2(x[i], x[i + 1]), make_float2(-r, -r)), make_float2(c, c));
+                acc0 += exp2_approx(y.x);
+                acc1 += exp2_approx(y.y);
+            } else {
+                acc0 += term(x[i], r, c);
+                if (i + 1 < N) acc1 += term(x[i + 1], r, c);
+            }
         }
         s = __fmaf_rn(s, term(m, r, c), acc0 + acc1);
         m = mn;
@@ -244,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
     const int64_t chunks = (p.V - head) / 8;
     const int64_t c0 = chunks * part / p.parts, c1 = chunks * (part + 1) / p.parts;
     Softmax2 acc{-INFINITY, 0.f};
-    constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : 6; // 96 bytes of loads in flight per thread: 174 us, 64 bytes 182
+    constexpr int kUnroll = DT_IN == QLORA_DTYPE_F32 ? 3 : 6; // bytes in flight per thread: 96, 166.6 us; 64, 172 ([4096, 128000] bf16)
     int64_t c = c0 + threadIdx.x;
     for (; c + (kUnroll - 1) * kThreads < c1; c += kUnroll * kThreads) {
         Raw8<DT_IN> raw[kUnroll];
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
         for (int u = 0; u < kUnroll; ++u) {
             float v[8];
             raw[u].values(v);
-            acc.add(v, p.c);
+            acc.add<DT_IN != QLORA_DTYPE_F32>(v, p.c);
         }
     }
     for (; c < c1; c += kThreads) {
@@ -262,13 +281,13 @@ __global__ void __launch_bounds__(kThreads, 5) distill_fwd(DistillParams p) {
         raw.load(row, head + 8 * c);
         float v[8];
         raw.values(v);
-        acc.add(v, p.c);
+        acc.add<DT_IN != QLORA_DTYPE_F32>(v, p.c);
     }
     if (part == p.parts - 1) {                                // fewer than 8 + 8 single elements
         const int64_t tail0 = head + 8 * chunks, singles = head + (p.V - tail0);
         if (threadIdx.x < singles) {
             const float v[1] = {load1<DT_IN>(row, threadIdx.x < head ? threadIdx.x : tail0 + (threadIdx.x - head))};
-            acc.add(v, p.c);
+            acc.add<false>(v, p.c);
         }
     }
 
