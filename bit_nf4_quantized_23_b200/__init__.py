@@ -42,39 +42,39 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _is_current(stream) -> bool:
-    return stream is None or stream.cuda_stream == torch.cuda.current_stream().cuda_stream
-
-
-def _allocating_on(stream):
-    """A context in which torch allocates for `stream` (None: the current one).  The caching allocator hands
-    out a block again in the order of the stream that it was allocated on, so memory that the kernels on
-    `stream` use has to come from there, or another call could have it while they still run."""
-    if _is_current(stream):
+# The caching allocator hands out a block again in the order of the stream that it was allocated on, so memory that
+# the kernels on another stream than the current one use has to come from there: another call could have it
+# while they still run.  Calls without `stream` use torch.empty itself.
+def _on(stream):
+    """A context in which torch allocates for `stream`."""
+    if stream.cuda_stream == torch.cuda.current_stream().cuda_stream:
         return contextlib.nullcontext()
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def _for_current(t: torch.Tensor, stream) -> torch.Tensor:
-    """An output allocated on `stream`, which the current stream is going to use too."""
-    if not _is_current(stream):
-        t.record_stream(torch.cuda.current_stream(t.device))
+    """An output allocated on `stream`, marked as used by the current stream, to which it is returned."""
+    current = torch.cuda.current_stream(t.device)
+    if stream.cuda_stream != current.cuda_stream:
+        t.record_stream(current)
     return t
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    if _is_current(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with _allocating_on(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _scratch(stream):
+    """torch.empty for memory that only the kernels on `stream` use."""
+    def empty(*shape, **kw):
+        with _on(stream):
+            return torch.empty(*shape, **kw)
+    return empty
 
 
-def _output(shape, dtype, device, stream) -> torch.Tensor:
-    if _is_current(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _allocating_on(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    return _for_current(t, stream)
+def _outputs(stream):
+    """torch.empty for what the kernels on `stream` write and the call returns."""
+    def empty(*shape, **kw):
+        with _on(stream):
+            t = torch.empty(*shape, **kw)
+        return _for_current(t, stream)
+    return empty
 
 
 def _ptr(t):
@@ -212,13 +212,14 @@ def qlora_quantize_nf4_dq(W: torch.Tensor, blocksize: int = 64, blocksize2: int 
     N, K = W.shape
     sizes = qlora_nf4_sizes(N, K, blocksize, blocksize2)
     if out is None:
-        with _allocating_on(stream):
+        with _on(stream) if stream is not None else contextlib.nullcontext():
             out = NF4Weight.empty(N, K, W.device, codebook, double_quant, compute_dtype)
-        for name in out._BUFFERS:
+        for name in out._BUFFERS if stream is not None else ():
             if getattr(out, name) is not None:
                 _for_current(getattr(out, name), stream)
     if workspace is None:
-        workspace = _scratch(sizes["workspace"], W.device, stream)
+        empty = torch.empty if stream is None else _scratch(stream)
+        workspace = empty(sizes["workspace"], dtype=torch.uint8, device=W.device)
     ws = out.c_struct()
     check(lib().qlora_quantize_nf4_dq(_ptr(W), N, K, blocksize, blocksize2, byref(ws), _ptr(workspace),
                                       workspace.numel(), _stream(stream)), "qlora_quantize_nf4_dq")
@@ -238,8 +239,9 @@ def qlora_quantize_nf4_dq_noalloc(W: torch.Tensor, out: NF4Weight, stream=None) 
 
 
 def qlora_dequantize(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output((w.N, w.K), w.compute_dtype, w.codes.device, stream)
+        out = empty(w.N, w.K, dtype=w.compute_dtype, device=w.codes.device)
     _need(out, w.compute_dtype, "out", (w.N, w.K))
     ws = w.c_struct()
     check(lib().qlora_dequantize(byref(ws), _ptr(out), _stream(stream)), "qlora_dequantize")
@@ -253,10 +255,11 @@ def qlora_quantize_int8_absmax(W: torch.Tensor, blocksize: int = 64, codes: torc
     Returns (codes int8 shaped like W, alpha fp32 [W.numel() // blocksize])."""
     _need(W, torch.bfloat16, "W")
     n = W.numel()
+    empty = torch.empty if stream is None else _outputs(stream)
     if codes is None:
-        codes = _output(W.shape, torch.int8, W.device, stream)
+        codes = empty(W.shape, dtype=torch.int8, device=W.device)
     if alpha is None:
-        alpha = _output((max(n // blocksize, 1),), torch.float32, W.device, stream)
+        alpha = empty(max(n // blocksize, 1), dtype=torch.float32, device=W.device)
     _need(codes, torch.int8, "codes", tuple(W.shape))
     _need(alpha, torch.float32, "alpha")
     if blocksize <= 0 or alpha.numel() * blocksize != n:
@@ -273,8 +276,9 @@ def qlora_dequantize_int8_absmax(codes: torch.Tensor, alpha: torch.Tensor, block
     _need(alpha, torch.float32, "alpha")
     if blocksize <= 0 or alpha.numel() * blocksize != codes.numel():
         raise ValueError(f"alpha must hold codes.numel() / blocksize = {codes.numel() // max(blocksize, 1)} scales")
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output(codes.shape, dtype, codes.device, stream)
+        out = empty(codes.shape, dtype=dtype, device=codes.device)
     _need(out, dtype, "out", tuple(codes.shape))
     check(lib().qlora_dequantize_int8_absmax(_ptr(codes), _ptr(alpha), codes.numel(), blocksize, _ptr(out),
                                              _dtype_code(dtype), _stream(stream)), "qlora_dequantize_int8_absmax")
@@ -287,8 +291,9 @@ def qlora_merge_lora(w: NF4Weight, A: torch.Tensor, B: torch.Tensor, r: int, alp
     qlora_quantize_nf4_dq to serve the merged model in 4 bits."""
     _need(A, w.compute_dtype, "A", (r, w.K))
     _need(B, w.compute_dtype, "B", (w.N, r))
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output((w.N, w.K), w.compute_dtype, w.codes.device, stream)
+        out = empty(w.N, w.K, dtype=w.compute_dtype, device=w.codes.device)
     _need(out, w.compute_dtype, "out", (w.N, w.K))
     ws = w.c_struct()
     check(lib().qlora_merge_lora(byref(ws), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream)),
@@ -304,7 +309,10 @@ def qlora_linear_workspace_size(M: int, N: int, K: int, r: int) -> int:
 
 def _workspace(M, N, K, r, device, workspace, stream):
     need = qlora_linear_workspace_size(M, N, K, r)
-    return _scratch(max(need, 16), device, stream) if workspace is None else workspace
+    if workspace is None:
+        empty = torch.empty if stream is None else _scratch(stream)
+        workspace = empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace
 
 
 def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, r: int,
@@ -318,11 +326,12 @@ def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Te
     _need(X, w.compute_dtype, "X", (M, w.K))
     _need(A, w.compute_dtype, "A", (r, w.K))
     _need(B, w.compute_dtype, "B", (w.N, r))
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output((M, w.N), y_dtype, X.device, stream)
+        out = empty(M, w.N, dtype=y_dtype, device=X.device)
     _need(out, y_dtype, "Y", (M, w.N))
     if save_U and U_out is None:
-        U_out = _output((M, r), torch.float32, X.device, stream)
+        U_out = empty(M, r, dtype=torch.float32, device=X.device)
     if U_out is not None:
         _need(U_out, torch.float32, "U", (M, r))
     workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
@@ -347,10 +356,11 @@ def qlora_linear_fwd_multi(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor, B
     _need(A_all, w.compute_dtype, "A_all", (n_ad, r, w.K))
     _need(B_all, w.compute_dtype, "B_all", (n_ad, w.N, r))
     _need(adapter_idx, torch.int32, "adapter_idx", (M,))
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output((M, w.N), y_dtype, X.device, stream)
+        out = empty(M, w.N, dtype=y_dtype, device=X.device)
     _need(out, y_dtype, "Y", (M, w.N))
-    U = _output((M, r), torch.float32, X.device, stream) if save_U else None
+    U = empty(M, r, dtype=torch.float32, device=X.device) if save_U else None
     workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
     ws = w.c_struct()
     check(lib().qlora_linear_fwd_multi(byref(ws), _ptr(X), M, _ptr(A_all), _ptr(B_all), n_ad, _ptr(adapter_idx),
@@ -374,14 +384,15 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     _need(B, w.compute_dtype, "B", (w.N, r))
     if U_saved is not None:
         _need(U_saved, torch.float32, "U_saved", (M, r))
+    empty = torch.empty if stream is None else _outputs(stream)
     if need_dX and dX is None:
-        dX = _output((M, w.K), dx_dtype, X.device, stream)
+        dX = empty(M, w.K, dtype=dx_dtype, device=X.device)
     if dX is not None:
         _need(dX, dx_dtype, "dX", (M, w.K))
     if dA is None:
-        dA = _output((r, w.K), torch.float32, X.device, stream)
+        dA = empty(r, w.K, dtype=torch.float32, device=X.device)
     if dB is None:
-        dB = _output((w.N, r), torch.float32, X.device, stream)
+        dB = empty(w.N, r, dtype=torch.float32, device=X.device)
     _need(dA, torch.float32, "dA", (r, w.K))
     _need(dB, torch.float32, "dB", (w.N, r))
     workspace = _workspace(M, w.N, w.K, r, X.device, workspace, stream)
@@ -445,7 +456,8 @@ def _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, strea
     if w.codes.get_device() != dev:
         raise ValueError(f"the weight must be on the current CUDA device cuda:{dev}, got {w.codes.device}")
     if workspace is None:
-        workspace = _scratch(qlora_adapters_workspace_size(M, w.N, w.K, r, n), X.device, stream)
+        empty = torch.empty if stream is None else _scratch(stream)
+        workspace = empty(qlora_adapters_workspace_size(M, w.N, w.K, r, n), dtype=torch.uint8, device=X.device)
     elif not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
     elif workspace.get_device() != dev or not workspace.is_contiguous() or workspace.dtype != torch.uint8:
@@ -465,11 +477,12 @@ def qlora_linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor
     dev = _device_of(X, "X")
     M, n, r, at, workspace = _adapter_args(w, X, A_all, B_all, adapter_idx, scales, workspace, dev, stream)
     y_dtype = w.compute_dtype if y_dtype is None else y_dtype
+    empty = torch.empty if stream is None else _outputs(stream)
     if out is None:
-        out = _output((M, w.N), y_dtype, X.device, stream)
+        out = empty((M, w.N), dtype=y_dtype, device=X.device)
     y_at = _need_on(out, y_dtype, "Y", (M, w.N), dev)
     if save_U and U_out is None:
-        U_out = _output((M, r), torch.float32, X.device, stream)
+        U_out = empty((M, r), dtype=torch.float32, device=X.device)
     u_at = None if U_out is None else _need_on(U_out, torch.float32, "U", (M, r), dev)
     check(lib().qlora_linear_fwd_adapters(byref(w.c_struct()), at[0], M, at[1], at[2], n, at[3], r, at[4], y_at,
                                           _dtype_code(y_dtype), u_at, workspace.data_ptr(), workspace.numel(),
@@ -489,13 +502,14 @@ def qlora_linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A
     dx_dtype = w.compute_dtype if dx_dtype is None else dx_dtype
     dy_at = _need_on(dY, w.compute_dtype, "dY", (M, w.N), dev)
     u_at = None if U_saved is None else _need_on(U_saved, torch.float32, "U_saved", (M, r), dev)
+    empty = torch.empty if stream is None else _outputs(stream)
     if need_dX and dX is None:
-        dX = _output((M, w.K), dx_dtype, X.device, stream)
+        dX = empty((M, w.K), dtype=dx_dtype, device=X.device)
     dx_at = None if dX is None else _need_on(dX, dx_dtype, "dX", (M, w.K), dev)
     if dA is None:
-        dA = _output((n, r, w.K), torch.float32, X.device, stream)
+        dA = empty((n, r, w.K), dtype=torch.float32, device=X.device)
     if dB is None:
-        dB = _output((n, w.N, r), torch.float32, X.device, stream)
+        dB = empty((n, w.N, r), dtype=torch.float32, device=X.device)
     da_at = _need_on(dA, torch.float32, "dA", (n, r, w.K), dev)
     db_at = _need_on(dB, torch.float32, "dB", (n, w.N, r), dev)
     check(lib().qlora_linear_bwd_adapters(byref(w.c_struct()), at[0], dy_at, M, at[1], at[2], n, at[3], r, at[4], u_at,
@@ -527,9 +541,10 @@ def _rows(t: torch.Tensor, name: str, dev: int, shape=None):
 
 def _topk_args(logits, teacher_idx, teacher_logits, dev):
     z_code, ld = _rows(logits, "logits", dev)
-    for t, name in ((teacher_idx, "teacher_idx"), (teacher_logits, "teacher_logits")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+    if not isinstance(teacher_idx, torch.Tensor):
+        raise TypeError("teacher_idx must be a torch.Tensor")
+    if not isinstance(teacher_logits, torch.Tensor):
+        raise TypeError("teacher_logits must be a torch.Tensor")
     if teacher_idx.dim() != 2:
         raise ValueError("teacher_idx must be a 2-D tensor [M, k]")
     k = teacher_idx.shape[1]
@@ -551,10 +566,11 @@ def qlora_distill_topk_fwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
     dev = _device_of(logits, "logits")
     z_code, ld, k, t_code, i_at, t_at = _topk_args(logits, teacher_idx, teacher_logits, dev)
     M, V = logits.shape
+    empty = torch.empty if stream is None else _outputs(stream)
     if loss is None:
-        loss = _output((M,), torch.float32, logits.device, stream)
+        loss = empty(M, dtype=torch.float32, device=logits.device)
     if lse is None:
-        lse = _output((M,), torch.float32, logits.device, stream)
+        lse = empty(M, dtype=torch.float32, device=logits.device)
     check(lib().qlora_distill_topk_fwd(logits.data_ptr(), z_code, ld, M, V, i_at, t_at, t_code, k, temperature,
                                        _need_on(loss, torch.float32, "loss", (M,), dev),
                                        _need_on(lse, torch.float32, "lse", (M,), dev), _stream_on(stream, dev)),
@@ -572,8 +588,9 @@ def qlora_distill_topk_bwd(logits: torch.Tensor, teacher_idx: torch.Tensor, teac
     M, V = logits.shape
     lse_at = _need_on(lse, torch.float32, "lse", (M,), dev)
     dloss_at = _need_on(dloss, torch.float32, "dloss", (M,), dev)
+    empty = torch.empty if stream is None else _outputs(stream)
     if dlogits is None:
-        dlogits = _output((M, V), logits.dtype if d_dtype is None else d_dtype, logits.device, stream)
+        dlogits = empty((M, V), dtype=logits.dtype if d_dtype is None else d_dtype, device=logits.device)
     elif d_dtype is not None and dlogits.dtype != d_dtype:
         raise TypeError(f"dlogits must be {d_dtype}, got {dlogits.dtype}")
     d_code, ldd = _rows(dlogits, "dlogits", dev, (M, V))
