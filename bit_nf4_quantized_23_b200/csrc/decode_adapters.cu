@@ -14,7 +14,8 @@
 // per CTA (one CTA per SM), and every (tile, CTA) piece is a segment accumulated in TMEM and written as
 // an fp32 partial tile to slot tile + CTA.  The tensor cores' fp32 sums lose about 2^-27 of themselves at
 // each step, one way, so tiles of A_all rows, whose U must keep fp32 digits for the gradients, are cut
-// into pieces of 1024 of K, each with slots of its own.  rows_finish_U sums the adapters' tiles to U, tc_rows_fixup
+// into pieces of 1024 of K, each with slots of its own.  Tiles of W_hat rows are not: their sums are as long as a
+// CTA's share of the tile, which a Y in fp32 shows.  rows_finish_U sums the adapters' tiles to U, tc_rows_fixup
 // the others, adds the adapter term s_a U B_a^T on the tensor cores and writes Y.
 //
 // The expansion of the codes bounds the kernel (byte permutes, about three ALU operations a weight on a
@@ -22,9 +23,11 @@
 // weights per handshake, the codes' stages are freed as soon as they are in registers, and a unit takes
 // four MMAs and two copies.
 // Roles (608 threads): warp 0 TMA of the tokens (and A_all rows), warp 1 TMEM owner + MMA issuer, warp 2
-// TMA of the codes (a warp of its own: behind the token ring the codes came a unit too late, 106 against
-// 100 us a call at W[28672, 8192] and 112 tokens), warps 3-18 four groups of producer warps that take units in
+// TMA of the codes (a warp of its own: behind the token ring the codes came a unit too late, 6% of the forward at
+// W[28672, 8192] and 112 tokens), warps 3-18 four groups of producer warps that take units in
 // turn; groups 0 and 1 also run the epilogues of even and odd segments.
+//
+// Times below are of the whole forward, as CUDA graph replays over three weights in turn.
 //
 // A parity wait tells apart only neighbouring phases, so no role may come to a barrier two phases
 // behind: each group has a row stage and a code stage of its own, an accumulator belongs to one group's
@@ -560,7 +563,7 @@ __host__ __device__ inline FixLayout fix_layout(uint32_t images, uint32_t tokens
 // dst[m, 0 .. 64) = the sum of src[b, m, 0 .. 64) over the slots b < n, in order: I chunks of four columns
 // a thread and B slots of each in flight.  For a few tokens that spreads a tile's many slots over threads
 // that had no token (4 tokens, W[4096, 4096], the whole forward: 21.6 to 20.5 us); for many tokens of few slots
-// it is more chunks than slots (112 tokens, W[28672, 8192]: 99.5 to 98 us).
+// it is more chunks than slots (112 tokens, W[28672, 8192]: 101.3 to 97.5 us).
 template <int I, int B>
 __device__ __forceinline__ void sum_slots(const float* src, int64_t slot_floats, int n, int M, int t, char* dst) {
     for (int i0 = t; i0 < M * 16; i0 += 128 * I) {

@@ -108,6 +108,9 @@ __device__ __forceinline__ void load_lanes_off(const uint32_t* entry, uint32_t (
 // tokens use; each adds its LoRA steps with that adapter's B (forward) or A (dX) as operand B, and
 // its MMAs update only the accumulator rows of its own tokens (tcgen05.mma's output-lane mask), so
 // no operand is masked or copied and a token never meets another request's adapter.
+// A tile's accumulators take all of TMEM, so a sum over the frozen weight is one chain of MMAs unless the reduction
+// is split; it loses about 2^-26 of itself toward zero at each 16-wide step (K = 11008: 1e-5), which hides under
+// 16-bit outputs and shows in fp32 ones, as it does with one adapter.
 template <int NUM_ACC, bool DX, bool MULTI>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 tc_gemm_nf4(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmCodes,

@@ -291,8 +291,19 @@ qlora_status qlora_linear_bwd(const qlora_nf4_weight* w, const void* X, const vo
  *   U_save      optional device fp32 [M, r] for the backward (zeros without adapter).
  *   workspace   at least qlora_adapters_workspace_size bytes; its contents need not
  *               start at any value, and calls that overlap on the GPU need their own.
- * Neither other tokens nor other adapters change a token's results, Inf and NaN included.
- * In fp16, |s_a U| and |dU| have to stay below 65504, as activations do.
+ * No value of another token or of another adapter enters a token's results, Inf and NaN
+ * included.  Where fp32 sums are cut goes by the numbers of tokens and of adapters in use, so
+ * a token's last bits may differ between batches; the same call repeats bit for bit.
+ * U_save (and dA_all, dB_all) keep fp32 digits: sums are cut every 1024 products at most.
+ * Y (and dX), in fp32 too, may be one tensor-core sum over the whole reduction, which loses
+ * about 2^-26 of itself toward zero for every 16 products, as qlora_linear_fwd does (K = 11008:
+ * 1e-5).  s_a U (and dU) enter them as two 16-bit parts: good to 2^-17 of themselves
+ * in bf16, to 2^-22 and an absolute 2^-25 in fp16, where they have to stay
+ * below 65504, as activations do.
+ * For up to 16 tokens of one scale qlora_linear_fwd_multi does the same: for ranks up to 16
+ * the faster call on weights up to W[8192, 8192] (16 tokens, r 8: 16 and 32 us against
+ * 23 and 39 at W[4096, 4096] and W[8192, 8192]), several times slower at 64 (90 and 107 us
+ * against 27 and 44).
  * Other arguments as qlora_linear_fwd (adapter_idx and scales need 4-byte alignment).
  * Errors: QLORA_ERR_INVALID_ARG for n_adapters outside 1 .. 65535, QLORA_ERR_SHAPE
  * when n_adapters * N is above 2^31 - 513, and those of qlora_linear_fwd.

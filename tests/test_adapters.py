@@ -600,3 +600,48 @@ def test_what_is_no_tensor_is_a_type_error(monkeypatch):
             q4.qlora_linear_fwd_adapters(w, X, **args)
         with pytest.raises(TypeError, match=name + " must be a torch.Tensor"):
             q4.qlora_linear_bwd_adapters(w, X, dY, **args)
+
+
+@pytest.mark.gpu
+def test_fp32_results_lose_no_more_than_their_chains():
+    """The tensor cores cut each running fp32 sum toward zero, at most a step of 2^-23 and on average half of it,
+    once for every 16 products.  U, dA and dB are joined from sums of 64 such steps; Y and dX in fp32 are one chain
+    over the whole reduction when there are tiles enough for the GPU (the largest loss there is)."""
+    M, N, K, r = 2048, 11008, 4864, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(BF16)
+    w = q4.qlora_quantize_nf4_dq(rnd(N, K, std=0.02))
+    X, dY, A, B = rnd(M, K), rnd(M, N), rnd(1, r, K, std=K ** -0.5), torch.zeros(1, N, r, dtype=BF16, device="cuda")
+    idx, one = torch.zeros(M, dtype=torch.int32, device="cuda"), torch.ones(1, device="cuda")
+    Y, U = q4.qlora_linear_fwd_adapters(w, X, A, B, idx, one, y_dtype=F32)
+    dX, _, dB = q4.qlora_linear_bwd_adapters(w, X, dY, A, B, idx, one, U_saved=U, dx_dtype=F32)
+    W, m = q4.qlora_dequantize(w).double(), slice(0, 128)
+    for name, got, ref, steps in (("Y", Y[m], X[m].double() @ W.t(), K / 16), ("dX", dX[m], dY[m].double() @ W, N / 16),
+                                  ("U", U, X.double() @ A[0].double().t(), 64),
+                                  ("dB", dB[0], dY.double().t() @ U.double(), 64)):
+        loss = float(((ref - got.double()) * ref.sign()).sum() / ref.abs().sum())
+        assert abs(loss) <= steps * 2.0 ** -24, (name, loss)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [8, 100])
+def test_what_a_small_fp16_dU_is_worth_in_dX(r):
+    """dU of about 1e-5 enters dX as two halves of fp16, together off by at most 2^-25: a few thousandths of such a
+    dU, and far below fp16's smallest number in dX itself.  The weight is zero, so that dX is the adapter's term."""
+    c = Case(200, 136, 192, r, 3, "runs", dt=F16)
+    c.w = q4.qlora_quantize_nf4_dq(torch.zeros(136, 192, dtype=BF16, device="cuda"), compute_dtype=F16)
+    c.Wd = q4.qlora_dequantize(c.w).double().cpu()
+    assert torch.all(c.Wd == 0)
+    c.dY.mul_(1e-3)
+    c.B.mul_(1e-2)
+    ref, _ = c.reference()
+    dX, _, _ = c.bwd(dx_dtype=F32)
+    # on top: sums of N and of 2 r products of fp32, at most 2^-23 of their magnitudes a step
+    s, idx, mag = c.scales.double().cpu(), c.idx.cpu(), torch.zeros_like(ref["dX"])
+    floor = torch.zeros_like(mag)
+    for a in range(3):
+        m = (idx == a).nonzero()[:, 0]
+        A = c.A[a].double().cpu().abs()
+        mag[m] = s[a] * (c.dY[m].double().cpu().abs() @ c.B[a].double().cpu().abs()) @ A
+        floor[m] = 2.0 ** -25 * A.sum(0)
+    assert torch.all((dX.double().cpu() - ref["dX"]).abs() <= floor + 40 * 2.0 ** -23 * mag)
