@@ -645,3 +645,15 @@ def test_what_a_small_fp16_dU_is_worth_in_dX(r):
         mag[m] = s[a] * (c.dY[m].double().cpu().abs() @ c.B[a].double().cpu().abs()) @ A
         floor[m] = 2.0 ** -25 * A.sum(0)
     assert torch.all((dX.double().cpu() - ref["dX"]).abs() <= floor + 40 * 2.0 ** -23 * mag)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_dB_of_a_long_batch_keeps_fp32_digits(dt):
+    """One adapter with 2048 tokens.  32 steps of the tensor cores, each of which loses 2^-26 of the running sum,
+    are 5e-7; the three parts of U (2^-24) and four fp32 additions (2^-24 each, either way) stay below 2e-7."""
+    c = Case(2048, 520, 512, 16, 1, "one", dt=dt)
+    U = (c.X.double() @ c.A[0].double().t()).float()
+    _, _, dB = c.bwd(U_saved=U)
+    ref = float(c.scales[0]) * c.dY.double().t() @ U.double()
+    assert float((dB[0].double() - ref).norm() / ref.norm()) <= 7e-7
